@@ -280,6 +280,103 @@ moe_status moe_layer_backward_events(const void *x, const void *Wg, const void *
                                      size_t bwd_ws_bytes, cudaEvent_t *events, int n_events,
                                      cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------------
+ * Grouped linear operators: one projection per expert over the grouped rows, for
+ * experts of any form (moe_expert_ffn is the SwiGLU one), dense layers beside them
+ * (E == 1), and their training.  For a row r of group e
+ *     z_r = x_r W_e^T + b_e            y_r = act(z_r) + residual_r
+ * and, for an upstream gradient dy,
+ *     dz_r = dy_r act'(z_r)            (the residual's gradient is dy itself)
+ *     dx_r = dz_r W_e     dW_e = sum_r dz_r^T x_r     db_e = sum_r dz_r
+ * crackai "Mixtral of Experts", "Top-2 Routing in Detail": an expert is a feed-forward
+ * network of its own; the pages fix SwiGLU for Mixtral, these operators leave the form
+ * to the caller, between moe_permute and moe_combine.
+ *
+ * Groups: offsets [E + 1] int32 on the device, as moe_permute writes them; group e owns
+ * rows offsets[e] .. offsets[e+1]-1.  `offsets` may be NULL when E == 1: one group of
+ * all rows.  Groups may be empty.  Rows behind the last group (offsets[E] .. rows-1) are
+ * neither computed nor written, and what x, dy, residual and the checkpoint hold there
+ * -- infinities and NaN included -- reaches no result.
+ * Shapes: K and N multiples of 8, 1 <= E <= 32, any rows >= 0 (rows == 0 queues
+ * nothing, except that moe_grouped_linear_backward writes zero dW and db). */
+typedef enum {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1, /* max(z, 0) */
+    MOE_ACT_GELU = 2, /* z (1 + erf(z / sqrt 2)) / 2 */
+    MOE_ACT_SILU = 3  /* z / (1 + e^-z) */
+} moe_act;
+
+/* Bytes of workspace moe_grouped_linear and moe_grouped_linear_train need for this
+ * shape; never decreasing in rows.  Zero the workspace once before its first use: it
+ * holds a status word (offset 0, moe_device_status) and counters that every completed
+ * call leaves at zero (zero it again after MOE_DEV_FLAG_TIMEOUT).  Calls that may run at
+ * the same time -- on two streams, or in two captured graphs -- each need their own.
+ * Returns 0 for unsupported arguments. */
+size_t moe_grouped_linear_workspace_bytes(int rows, int K, int N, int E, moe_dtype dt);
+
+/* y_r = act(x_r W_e^T + b_e) + residual_r.
+ *   x        [rows, K]  dt in       W        [E, N, K]  dt in (K contiguous)
+ *   bias     [E, N]     dt in, or NULL
+ *   residual [rows, N]  dt in, or NULL; may be y itself when y_dt == dt
+ *   y        [rows, N]  y_dt out
+ * dt == MOE_BF16: tensor cores with fp32 accumulation, everything up to y in fp32 and
+ * one rounding to y_dt (MOE_BF16, or MOE_F32 as moe_combine reads it).  dt == MOE_F32:
+ * fp32 throughout on CUDA cores, y_dt == MOE_F32. */
+moe_status moe_grouped_linear(const void *x, const int32_t *offsets, const void *W,
+                              const void *bias, const void *residual, int rows, int K, int N,
+                              int E, moe_act act, moe_dtype dt, moe_dtype y_dt, void *y, void *ws,
+                              size_t ws_bytes, cudaStream_t stream);
+
+/* 8-bit activation checkpoint.  A row of N values is kept in blocks of
+ * MOE_CHECKPOINT_BLOCK consecutive ones (the last block may be shorter):
+ *   scale s = max|v| / 128, code q = floor(v / s) in [-128, 127], and q stands for
+ *   (q + 1/2) s:  codes [rows, N] int8, scales [rows, ceil(N / 32)] float.
+ * The value is off by at most s / 2 = max|v| / 256, and its sign is kept (v >= 0 gives
+ * q >= 0), so that a ReLU's mask survives.  A block whose largest magnitude is below
+ * 2^-100 is kept as zeros (s = 0); one that holds an infinity or NaN comes back as
+ * infinities or NaN. */
+#define MOE_CHECKPOINT_BLOCK 32
+
+/* moe_grouped_linear for training: the same y, and the pre-activations z kept as an
+ * 8-bit checkpoint (codes, scales) for moe_grouped_linear_backward: 1.125 bytes a
+ * value.  z is taken from the fp32 accumulator.  dt must be MOE_BF16
+ * (MOE_ERR_UNSUPPORTED otherwise). */
+moe_status moe_grouped_linear_train(const void *x, const int32_t *offsets, const void *W,
+                                    const void *bias, const void *residual, int rows, int K,
+                                    int N, int E, moe_act act, moe_dtype dt, moe_dtype y_dt,
+                                    void *y, int8_t *codes, float *scales, void *ws,
+                                    size_t ws_bytes, cudaStream_t stream);
+
+/* Keep any rows v [rows, N] (dt) as an 8-bit checkpoint (N a multiple of 8). */
+moe_status moe_checkpoint_save(const void *v, int rows, int N, moe_dtype dt, int8_t *codes,
+                               float *scales, cudaStream_t stream);
+
+/* out [rows, N] (out_dt) = act(value of each code), rounded once: with MOE_ACT_NONE the
+ * kept values themselves, else for example the next projection's input recomputed from
+ * this one's checkpoint. */
+moe_status moe_checkpoint_restore(const int8_t *codes, const float *scales, int rows, int N,
+                                  moe_act act, moe_dtype out_dt, void *out, cudaStream_t stream);
+
+/* Bytes of workspace moe_grouped_linear_backward needs (zeroing, sharing and the status
+ * word as for moe_grouped_linear_workspace_bytes); 0 for unsupported arguments. */
+size_t moe_grouped_linear_backward_workspace_bytes(int rows, int K, int N, int E, moe_dtype dt);
+
+/* Gradients of moe_grouped_linear_train for upstream gradient dy [rows, N] (dt):
+ *   codes, scales  the checkpoint of that call; NULL allowed when act == MOE_ACT_NONE,
+ *                  whose slope is 1 (then they are not read)
+ *   dx [rows, K]   dt out, or NULL
+ *   dW [E, N, K]   dw_dt out (MOE_BF16 or MOE_F32), or NULL; an expert without rows
+ *                  gets zeros
+ *   db [E, N]      float out, or NULL
+ * Outputs are overwritten.  dz is rounded once to bf16 for the tensor cores (db sums it
+ * unrounded, in fp32 and in a fixed order); products accumulate in fp32.  The same inputs
+ * give the same bits.  dt must be MOE_BF16 (MOE_ERR_UNSUPPORTED otherwise). */
+moe_status moe_grouped_linear_backward(const void *dy, const void *x, const int32_t *offsets,
+                                       const void *W, const int8_t *codes, const float *scales,
+                                       int rows, int K, int N, int E, moe_act act, moe_dtype dt,
+                                       moe_dtype dw_dt, void *dx, void *dW, float *db, void *ws,
+                                       size_t ws_bytes, cudaStream_t stream);
+
 /* Static description of a status code. */
 const char *moe_status_string(moe_status st);
 

@@ -9,7 +9,10 @@ package fails if the library has not been built.
 Entry points (same names as the C ABI):
     moe_route, moe_permute, moe_expert_ffn, moe_combine, moe_layer_forward,
     moe_workspace_bytes, moe_device_status, moe_status_string
-plus the conveniences ``alloc_workspace`` and ``layer_forward``.
+plus the conveniences ``alloc_workspace`` and ``layer_forward``; and the grouped linear
+operators for experts of any form (``moe_grouped_linear``, its training form with an
+8-bit checkpoint, ``moe_grouped_linear_backward``, ``moe_checkpoint_save`` and
+``moe_checkpoint_restore``).
 """
 from __future__ import annotations
 
@@ -26,6 +29,11 @@ __all__ = [
     "moe_layer_forward_capacity", "moe_selftest_wait_timeout", "moe_backward_workspace_bytes",
     "moe_layer_backward", "alloc_backward_workspace", "layer_backward",
     "moe_layer_backward_events", "moe_layer_forward_train",
+    "moe_grouped_linear_workspace_bytes", "moe_grouped_linear", "moe_grouped_linear_train",
+    "moe_grouped_linear_backward_workspace_bytes", "moe_grouped_linear_backward",
+    "moe_checkpoint_save", "moe_checkpoint_restore", "alloc_grouped_linear_workspace",
+    "alloc_grouped_linear_backward_workspace", "alloc_checkpoint", "grouped_linear",
+    "CHECKPOINT_BLOCK",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe.so")
@@ -38,7 +46,13 @@ EXPORTED_SYMBOLS = ("moe_workspace_bytes", "moe_route", "moe_permute", "moe_expe
                     "moe_device_status", "moe_status_string", "moe_expert_ffn_static",
                     "moe_layer_forward_capacity", "moe_selftest_wait_timeout",
                     "moe_backward_workspace_bytes", "moe_layer_backward",
-                    "moe_layer_backward_events", "moe_layer_forward_train")
+                    "moe_layer_backward_events", "moe_layer_forward_train",
+                    "moe_grouped_linear_workspace_bytes", "moe_grouped_linear",
+                    "moe_grouped_linear_train", "moe_grouped_linear_backward_workspace_bytes",
+                    "moe_grouped_linear_backward", "moe_checkpoint_save",
+                    "moe_checkpoint_restore")
+
+
 def launches_per_layer(T: int, d: int = 4096, E: int = 8, bf16: bool = True) -> int:
     """Kernels one moe_layer_forward queues: router 1, permutation 1 (T <= 512) or 4
     (count, scan, rank, gather; 3 where the bf16 fp64-tensor-core router counts the
@@ -100,6 +114,13 @@ def _load() -> ctypes.CDLL:
         "moe_layer_backward_events": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
                                             i32, vp, vp, vp, vp, vp, vp, sz, vp, sz, vp, i32,
                                             vp]),
+        "moe_grouped_linear_workspace_bytes": (sz, [i32] * 5),
+        "moe_grouped_linear": (i32, [vp] * 5 + [i32] * 7 + [vp, vp, sz, vp]),
+        "moe_grouped_linear_train": (i32, [vp] * 5 + [i32] * 7 + [vp, vp, vp, vp, sz, vp]),
+        "moe_grouped_linear_backward_workspace_bytes": (sz, [i32] * 5),
+        "moe_grouped_linear_backward": (i32, [vp] * 6 + [i32] * 7 + [vp, vp, vp, vp, sz, vp]),
+        "moe_checkpoint_save": (i32, [vp, i32, i32, i32, vp, vp, vp]),
+        "moe_checkpoint_restore": (i32, [vp, vp, i32, i32, i32, i32, vp, vp]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
@@ -444,3 +465,179 @@ def layer_backward(x, Wg, W1, W3, W2, dy, fwd_ws, capacity: int = -1, bwd_ws=Non
     dW3, dW2 = torch.empty(W3.shape, **f32), torch.empty(W2.shape, **f32)
     moe_layer_backward(x, Wg, W1, W3, W2, dy, dx, dWg, dW1, dW3, dW2, fwd_ws, bwd_ws, capacity)
     return dx, dWg, dW1, dW3, dW2
+
+
+# ------------------------------------------------------------------ grouped linear
+CHECKPOINT_BLOCK = 32
+_ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+
+
+def _act(act: str) -> int:
+    try:
+        return _ACTS[act]
+    except (KeyError, TypeError):
+        raise ValueError(f"act: {act!r}, expected one of {sorted(_ACTS)}") from None
+
+
+def _dt_of(dtype: torch.dtype) -> int:
+    if dtype == torch.bfloat16:
+        return MOE_BF16
+    if dtype == torch.float32:
+        return MOE_F32
+    raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
+
+
+def moe_grouped_linear_workspace_bytes(rows: int, K: int, N: int, E: int,
+                                       dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(_lib.moe_grouped_linear_workspace_bytes(rows, K, N, E, _dt_of(dtype)))
+
+
+def moe_grouped_linear_backward_workspace_bytes(rows: int, K: int, N: int, E: int,
+                                                dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(_lib.moe_grouped_linear_backward_workspace_bytes(rows, K, N, E, _dt_of(dtype)))
+
+
+def alloc_grouped_linear_workspace(rows: int, K: int, N: int, E: int,
+                                   dtype: torch.dtype = torch.bfloat16,
+                                   device="cuda") -> torch.Tensor:
+    """A zeroed workspace for ``moe_grouped_linear`` and ``moe_grouped_linear_train``."""
+    n = moe_grouped_linear_workspace_bytes(rows, K, N, E, dtype)
+    if n == 0:
+        raise MoeError("moe_grouped_linear_workspace_bytes", 2, "unsupported shape")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def alloc_grouped_linear_backward_workspace(rows: int, K: int, N: int, E: int,
+                                            dtype: torch.dtype = torch.bfloat16,
+                                            device="cuda") -> torch.Tensor:
+    """A zeroed workspace for ``moe_grouped_linear_backward``."""
+    n = moe_grouped_linear_backward_workspace_bytes(rows, K, N, E, dtype)
+    if n == 0:
+        raise MoeError("moe_grouped_linear_backward_workspace_bytes", 2, "unsupported shape")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def alloc_checkpoint(rows: int, N: int, device="cuda"):
+    """(codes, scales) buffers of an 8-bit checkpoint of [rows, N] values."""
+    nb = (N + CHECKPOINT_BLOCK - 1) // CHECKPOINT_BLOCK
+    return (torch.empty(rows, N, dtype=torch.int8, device=device),
+            torch.empty(rows, nb, dtype=torch.float32, device=device))
+
+
+def _check_checkpoint(codes, scales, rows: int, N: int) -> None:
+    _expect("codes", codes, (rows, N), torch.int8)
+    _expect("scales", scales, (rows, (N + CHECKPOINT_BLOCK - 1) // CHECKPOINT_BLOCK),
+            torch.float32)
+
+
+def _linear_dims(x, offsets, W, bias):
+    if x.dim() != 2 or W.dim() != 3:
+        raise ValueError("x must be [rows, K] and W [E, N, K]")
+    rows, K = x.shape
+    E, N, _ = W.shape
+    dt = _dt(x)
+    _expect("W", W, (E, N, K), x.dtype)
+    if offsets is None:
+        if E != 1:
+            raise ValueError("offsets may be None only with one expert")
+    else:
+        _expect_numel("offsets", offsets, E + 1, torch.int32)
+    if bias is not None:
+        _expect("bias", bias, (E, N), x.dtype)
+    return rows, K, N, E, dt
+
+
+def _linear(fn, x, offsets, W, y, ws, bias, residual, act, codes, scales, stream) -> None:
+    rows, K, N, E, dt = _linear_dims(x, offsets, W, bias)
+    _expect("y", y, (rows, N))
+    y_dt = _dt(y)
+    if residual is not None:
+        _expect("residual", residual, (rows, N), x.dtype)
+    _ws("ws", ws)
+    tensors = [t for t in (x, offsets, W, y, ws, bias, residual, codes, scales) if t is not None]
+    kept = () if codes is None else (_ptr(codes), _ptr(scales))
+    with torch.cuda.device(_dev(*tensors)):
+        _check(fn, getattr(_lib, fn)(_ptr(x), _ptr(offsets), _ptr(W), _ptr(bias), _ptr(residual),
+                                     rows, K, N, E, _act(act), dt, y_dt, _ptr(y), *kept, _ptr(ws),
+                                     ws.numel(), _stream(stream)))
+
+
+def moe_grouped_linear(x, offsets, W, y, ws, bias=None, residual=None, act: str = "none",
+                       stream=None) -> None:
+    """``y_r = act(x_r W_e^T + b_e) + residual_r`` for every row r of expert e's group.
+    ``offsets`` may be None with one expert; ``act`` is "none", "relu", "gelu" or "silu"."""
+    _linear("moe_grouped_linear", x, offsets, W, y, ws, bias, residual, act, None, None, stream)
+
+
+def moe_grouped_linear_train(x, offsets, W, y, codes, scales, ws, bias=None, residual=None,
+                             act: str = "none", stream=None) -> None:
+    """``moe_grouped_linear`` that also keeps the pre-activation in 8 bits (``codes``,
+    ``scales`` as from ``alloc_checkpoint``) for ``moe_grouped_linear_backward``."""
+    if x.dim() == 2 and W.dim() == 3:
+        _check_checkpoint(codes, scales, x.shape[0], W.shape[1])
+    _linear("moe_grouped_linear_train", x, offsets, W, y, ws, bias, residual, act, codes, scales,
+            stream)
+
+
+def grouped_linear(x, offsets, W, bias=None, residual=None, act: str = "none", ws=None, out=None,
+                   stream=None) -> torch.Tensor:
+    """``moe_grouped_linear``, allocating the workspace and output with torch if not given."""
+    if ws is None:
+        ws = alloc_grouped_linear_workspace(x.shape[0], x.shape[1], W.shape[1], W.shape[0],
+                                            x.dtype, x.device)
+    if out is None:
+        out = torch.empty(x.shape[0], W.shape[1], dtype=x.dtype, device=x.device)
+    moe_grouped_linear(x, offsets, W, out, ws, bias, residual, act, stream)
+    return out
+
+
+def moe_checkpoint_save(v, codes, scales, stream=None) -> None:
+    """Keep rows ``v [rows, N]`` as an 8-bit checkpoint."""
+    if v.dim() != 2:
+        raise ValueError("v must be [rows, N]")
+    rows, N = v.shape
+    _check_checkpoint(codes, scales, rows, N)
+    dt = _dt(v)
+    with torch.cuda.device(_dev(v, codes, scales)):
+        _check("moe_checkpoint_save", _lib.moe_checkpoint_save(
+            _ptr(v), rows, N, dt, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def moe_checkpoint_restore(codes, scales, out, act: str = "none", stream=None) -> None:
+    """``out [rows, N] = act(value of each code)``, rounded once to ``out``'s dtype."""
+    if out.dim() != 2:
+        raise ValueError("out must be [rows, N]")
+    rows, N = out.shape
+    _check_checkpoint(codes, scales, rows, N)
+    dt = _dt(out)
+    with torch.cuda.device(_dev(codes, scales, out)):
+        _check("moe_checkpoint_restore", _lib.moe_checkpoint_restore(
+            _ptr(codes), _ptr(scales), rows, N, _act(act), dt, _ptr(out), _stream(stream)))
+
+
+def moe_grouped_linear_backward(dy, x, offsets, W, ws, dx=None, dW=None, db=None, codes=None,
+                                scales=None, act: str = "none", stream=None) -> None:
+    """Gradients of ``moe_grouped_linear_train`` for upstream gradient ``dy``: any of ``dx``
+    (x's dtype), ``dW`` (bf16 or fp32) and ``db`` (fp32) that is given is overwritten.
+    ``codes`` and ``scales`` may be left out with ``act="none"``."""
+    rows, K, N, E, dt = _linear_dims(x, offsets, W, None)
+    _expect("dy", dy, (rows, N), x.dtype)
+    if dx is not None:
+        _expect("dx", dx, (rows, K), x.dtype)
+    dw_dt = dt
+    if dW is not None:
+        _expect("dW", dW, (E, N, K))
+        dw_dt = _dt(dW)
+    if db is not None:
+        _expect("db", db, (E, N), torch.float32)
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales go together")
+    if codes is not None:
+        _check_checkpoint(codes, scales, rows, N)
+    _ws("ws", ws)
+    tensors = [t for t in (dy, x, offsets, W, ws, dx, dW, db, codes, scales) if t is not None]
+    with torch.cuda.device(_dev(*tensors)):
+        _check("moe_grouped_linear_backward", _lib.moe_grouped_linear_backward(
+            _ptr(dy), _ptr(x), _ptr(offsets), _ptr(W), _ptr(codes), _ptr(scales), rows, K, N, E,
+            _act(act), dt, dw_dt, _ptr(dx), _ptr(dW), _ptr(db), _ptr(ws), ws.numel(),
+            _stream(stream)))

@@ -1,0 +1,245 @@
+// grouped_linear.cu -- the grouped linear operators on CUDA cores: plain tiled kernels
+// that are right for every shape.
+//
+// A block computes a 64 x 64 tile of the output of one group with 256 threads, 4 x 4
+// values each, over steps of 16 of the reduction staged in shared memory as fp32.
+#include <cuda_bf16.h>
+
+#include "act_checkpoint.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kT = 64;       // tile side
+constexpr int kStep = 16;    // reduction per step
+constexpr int kThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v) {
+    return static_cast<float>(v);
+}
+
+// Tile `y` of the row tiles of all groups -> group e, first row, end row.
+__device__ __forceinline__ bool row_tile(const int* off, int E, int y, int& e, int& row0,
+                                         int& row_end) {
+    for (int g = 0; g < E; ++g) {
+        const int t = (off[g + 1] - off[g] + kT - 1) / kT;
+        if (y < t) {
+            e = g;
+            row0 = off[g] + y * kT;
+            row_end = off[g + 1];
+            return true;
+        }
+        y -= t;
+    }
+    return false;
+}
+
+// acc[i][j] += sum_c A(m0 + .., c) B(n0 + .., c): fa / fb read one operand value, 0
+// outside.
+template <typename FA, typename FB>
+__device__ __forceinline__ void tile_product(int C, FA fa, FB fb, float (&acc)[4][4]) {
+    __shared__ float sa[kStep][kT + 1], sb[kStep][kT + 1];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    for (int c0 = 0; c0 < C; c0 += kStep) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < kStep * kT; i += kThreads) {
+            const int c = i % kStep, m = i / kStep;
+            sa[c][m] = c0 + c < C ? fa(m, c0 + c) : 0.f;
+            sb[c][m] = c0 + c < C ? fb(m, c0 + c) : 0.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < kStep; ++c) {
+            float a[4], b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = sa[c][ty * 4 + i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b[j] = sb[c][tx + 16 * j];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+        }
+    }
+}
+
+template <typename T, typename TY>
+__global__ void __launch_bounds__(kThreads) linear_kernel(const LinearArgs a) {
+    __shared__ int off[kMaxExperts + 1];
+    __shared__ float sz[kT][kT + 1];
+    if (threadIdx.x == 0) load_group_bounds(a.offsets, a.E, a.rows, off);
+    __syncthreads();
+    int e, row0, row_end;
+    if (!row_tile(off, a.E, blockIdx.y, e, row0, row_end)) return;
+    const int n0 = blockIdx.x * kT;
+    const T* x = static_cast<const T*>(a.x);
+    const T* W = static_cast<const T*>(a.W) + static_cast<size_t>(e) * a.N * a.K;
+    float acc[4][4] = {};
+    tile_product(
+        a.K,
+        [&](int m, int c) {
+            return row0 + m < row_end ? to_f32(x[static_cast<size_t>(row0 + m) * a.K + c]) : 0.f;
+        },
+        [&](int n, int c) {
+            return n0 + n < a.N ? to_f32(W[static_cast<size_t>(n0 + n) * a.K + c]) : 0.f;
+        },
+        acc);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sz[ty * 4 + i][tx + 16 * j] = acc[i][j];
+    __syncthreads();
+    // eight consecutive outputs per thread: 8 threads a row, 32 rows at a time
+    const int f = (threadIdx.x & 7) * 8, n = n0 + f;
+    for (int m = threadIdx.x >> 3; m < kT; m += kThreads / 8) {
+        const int row = row0 + m;
+        const bool valid = row < row_end && n < a.N;
+        float z[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) z[k] = valid ? sz[m][f + k] : 0.f;
+        if (valid && a.bias) {
+            float b[8];
+            load8(static_cast<const T*>(a.bias) + static_cast<size_t>(e) * a.N + n, b);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) z[k] += b[k];
+        }
+        if (a.codes) {
+            uint32_t mag = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mag = max(mag, ckpt_mag(z[k]));
+            mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+            mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+            const float s = ckpt_scale(mag);
+            if (valid) {
+                *reinterpret_cast<uint2*>(a.codes + static_cast<size_t>(row) * a.N + n) =
+                    ckpt_pack8(z, s);
+                if ((threadIdx.x & 3) == 0)
+                    a.scales[static_cast<size_t>(row) * ckpt_blocks(a.N) + n / kCkptBlock] = s;
+            }
+        }
+        if (!valid) continue;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) z[k] = act_value(a.act, z[k]);
+        if (a.residual) {
+            float r[8];
+            load8(static_cast<const T*>(a.residual) + static_cast<size_t>(row) * a.N + n, r);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) z[k] += r[k];
+        }
+        store8(static_cast<TY*>(a.y) + static_cast<size_t>(row) * a.N + n, z);
+    }
+}
+
+// dz = dy act'(value of the code), and db = sum of dz over the group's rows, fp32.
+__global__ void __launch_bounds__(kThreads) linear_dz_kernel(const LinearBwdArgs a) {
+    __shared__ int off[kMaxExperts + 1];
+    if (threadIdx.x == 0) load_group_bounds(a.offsets, a.E, a.rows, off);
+    __syncthreads();
+    const int e = blockIdx.y, n = (blockIdx.x * kThreads + threadIdx.x) * 8;
+    if (n >= a.N) return;
+    const int nb = ckpt_blocks(a.N);
+    float sum[8] = {};
+    for (int r = off[e]; r < off[e + 1]; ++r) {
+        const size_t at = static_cast<size_t>(r) * a.N + n;
+        float g[8];
+        load8(static_cast<const __nv_bfloat16*>(a.dy) + at, g);
+        if (a.codes) {
+            float z[8];
+            ckpt_unpack8(*reinterpret_cast<const uint2*>(a.codes + at),
+                         a.scales[static_cast<size_t>(r) * nb + n / kCkptBlock], z);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) g[k] *= act_slope(a.act, z[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[k] += g[k];
+        store8(static_cast<__nv_bfloat16*>(a.dz) + at, g);
+    }
+    if (a.db) store8(a.db + static_cast<size_t>(e) * a.N + n, sum);
+}
+
+__global__ void __launch_bounds__(kThreads) linear_dx_kernel(const LinearBwdArgs a) {
+    __shared__ int off[kMaxExperts + 1];
+    if (threadIdx.x == 0) load_group_bounds(a.offsets, a.E, a.rows, off);
+    __syncthreads();
+    int e, row0, row_end;
+    if (!row_tile(off, a.E, blockIdx.y, e, row0, row_end)) return;
+    const int k0 = blockIdx.x * kT;
+    const auto* dz = static_cast<const __nv_bfloat16*>(a.dz);
+    const auto* W =
+        static_cast<const __nv_bfloat16*>(a.W) + static_cast<size_t>(e) * a.N * a.K;
+    float acc[4][4] = {};
+    tile_product(
+        a.N,
+        [&](int m, int c) {
+            return row0 + m < row_end ? to_f32(dz[static_cast<size_t>(row0 + m) * a.N + c]) : 0.f;
+        },
+        [&](int k, int c) {
+            return k0 + k < a.K ? to_f32(W[static_cast<size_t>(c) * a.K + k0 + k]) : 0.f;
+        },
+        acc);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j)
+            if (row0 + ty * 4 + i < row_end && k0 + tx + 16 * j < a.K)
+                static_cast<__nv_bfloat16*>(
+                    a.dx)[static_cast<size_t>(row0 + ty * 4 + i) * a.K + k0 + tx + 16 * j] =
+                    __float2bfloat16_rn(acc[i][j]);
+}
+
+template <typename TW>
+__global__ void __launch_bounds__(kThreads) linear_dw_kernel(const LinearBwdArgs a) {
+    __shared__ int off[kMaxExperts + 1];
+    if (threadIdx.x == 0) load_group_bounds(a.offsets, a.E, a.rows, off);
+    __syncthreads();
+    const int e = blockIdx.z, n0 = blockIdx.y * kT, k0 = blockIdx.x * kT;
+    const int r0 = off[e];
+    const auto* dz = static_cast<const __nv_bfloat16*>(a.dz);
+    const auto* x = static_cast<const __nv_bfloat16*>(a.x);
+    float acc[4][4] = {};
+    tile_product(
+        off[e + 1] - r0,
+        [&](int n, int c) {
+            return n0 + n < a.N ? to_f32(dz[static_cast<size_t>(r0 + c) * a.N + n0 + n]) : 0.f;
+        },
+        [&](int k, int c) {
+            return k0 + k < a.K ? to_f32(x[static_cast<size_t>(r0 + c) * a.K + k0 + k]) : 0.f;
+        },
+        acc);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j) {
+            const int n = n0 + ty * 4 + i, k = k0 + tx + 16 * j;
+            if (n < a.N && k < a.K)
+                static_cast<TW*>(a.dW)[(static_cast<size_t>(e) * a.N + n) * a.K + k] =
+                    static_cast<TW>(acc[i][j]);
+        }
+}
+
+unsigned blocks(int n) { return static_cast<unsigned>((n + kT - 1) / kT); }
+
+}  // namespace
+
+cudaError_t launch_linear(const LinearArgs& a) {
+    const dim3 grid(blocks(a.N), blocks(a.rows) + a.E);
+    auto kern = a.dt == MOE_F32      ? linear_kernel<float, float>
+                : a.y_dt == MOE_F32 ? linear_kernel<__nv_bfloat16, float>
+                                    : linear_kernel<__nv_bfloat16, __nv_bfloat16>;
+    return launch_k(kern, grid, kThreads, 0, a.stream, a);
+}
+
+cudaError_t launch_linear_backward(const LinearBwdArgs& a) {
+    cudaError_t err =
+        launch_k(linear_dz_kernel, dim3((a.N / 8 + kThreads - 1) / kThreads, a.E), kThreads, 0,
+                 a.stream, a);
+    if (err == cudaSuccess && a.dx)
+        err = launch_k(linear_dx_kernel, dim3(blocks(a.K), blocks(a.rows) + a.E), kThreads, 0,
+                       a.stream, a);
+    if (err == cudaSuccess && a.dW)
+        err = launch_k(a.dw_dt == MOE_F32 ? linear_dw_kernel<float> : linear_dw_kernel<__nv_bfloat16>,
+                       dim3(blocks(a.K), blocks(a.N), a.E), kThreads, 0, a.stream, a);
+    return err;
+}
+
+}  // namespace moe

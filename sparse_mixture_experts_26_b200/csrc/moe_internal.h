@@ -289,4 +289,49 @@ cudaError_t launch_selftest_wait(uint32_t* status, uint32_t* scratch, unsigned l
 cudaError_t launch_sum_splits(const float* parts, int nsplit, size_t n, float* Y,
                               cudaStream_t s);
 
+
+// ---- grouped linear operators (include/moe.h)
+// Forward: y_r = act(x_r W_e^T + b_e) + residual_r; with codes / scales the
+// pre-activation is also kept in 8 bits.  K: reduction length, N: outputs.
+struct LinearArgs {
+    const void* x;
+    const int32_t* offsets;  // nullptr: one group of all rows
+    const void* W;
+    const void* bias;        // or nullptr
+    const void* residual;    // or nullptr
+    int rows, K, N, E;
+    int act;
+    moe_dtype dt, y_dt;
+    void* y;
+    int8_t* codes;           // or nullptr
+    float* scales;
+    uint32_t* status;
+    cudaStream_t stream;
+};
+cudaError_t launch_linear(const LinearArgs& a);
+
+// Backward; W [E, N, K] as in the forward.
+struct LinearBwdArgs {
+    const void* dy;
+    const void* x;
+    const int32_t* offsets;
+    const void* W;
+    const int8_t* codes;     // nullptr: slope 1
+    const float* scales;
+    int rows, K, N, E;
+    int act;
+    moe_dtype dw_dt;
+    void* dx;                // or nullptr
+    void* dW;                // or nullptr
+    float* db;               // or nullptr
+    void* dz;                // bf16 [rows, N] scratch
+    uint32_t* status;
+    cudaStream_t stream;
+};
+cudaError_t launch_linear_backward(const LinearBwdArgs& a);
+cudaError_t launch_checkpoint_save(const void* v, int rows, int N, moe_dtype dt, int8_t* codes,
+                                   float* scales, cudaStream_t s);
+cudaError_t launch_checkpoint_restore(const int8_t* codes, const float* scales, int rows, int N,
+                                      int act, moe_dtype out_dt, void* out, cudaStream_t s);
+
 }  // namespace moe

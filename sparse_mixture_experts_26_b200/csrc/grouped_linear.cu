@@ -159,35 +159,6 @@ __global__ void __launch_bounds__(kThreads) linear_dz_kernel(const LinearBwdArgs
     if (a.db) store8(a.db + static_cast<size_t>(e) * a.N + n, sum);
 }
 
-__global__ void __launch_bounds__(kThreads) linear_dx_kernel(const LinearBwdArgs a) {
-    __shared__ int off[kMaxExperts + 1];
-    if (threadIdx.x == 0) load_group_bounds(a.offsets, a.E, a.rows, off);
-    __syncthreads();
-    int e, row0, row_end;
-    if (!row_tile(off, a.E, blockIdx.y, e, row0, row_end)) return;
-    const int k0 = blockIdx.x * kT;
-    const auto* dz = static_cast<const __nv_bfloat16*>(a.dz);
-    const auto* W =
-        static_cast<const __nv_bfloat16*>(a.W) + static_cast<size_t>(e) * a.N * a.K;
-    float acc[4][4] = {};
-    tile_product(
-        a.N,
-        [&](int m, int c) {
-            return row0 + m < row_end ? to_f32(dz[static_cast<size_t>(row0 + m) * a.N + c]) : 0.f;
-        },
-        [&](int k, int c) {
-            return k0 + k < a.K ? to_f32(W[static_cast<size_t>(c) * a.K + k0 + k]) : 0.f;
-        },
-        acc);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j)
-            if (row0 + ty * 4 + i < row_end && k0 + tx + 16 * j < a.K)
-                static_cast<__nv_bfloat16*>(
-                    a.dx)[static_cast<size_t>(row0 + ty * 4 + i) * a.K + k0 + tx + 16 * j] =
-                    __float2bfloat16_rn(acc[i][j]);
-}
-
 template <typename TW>
 __global__ void __launch_bounds__(kThreads) linear_dw_kernel(const LinearBwdArgs a) {
     __shared__ int off[kMaxExperts + 1];
@@ -222,20 +193,32 @@ unsigned blocks(int n) { return static_cast<unsigned>((n + kT - 1) / kT); }
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs& a) {
+    if (a.dt == MOE_BF16) return launch_linear_bf16(a, /*transposed=*/false);
     const dim3 grid(blocks(a.N), blocks(a.rows) + a.E);
-    auto kern = a.dt == MOE_F32      ? linear_kernel<float, float>
-                : a.y_dt == MOE_F32 ? linear_kernel<__nv_bfloat16, float>
-                                    : linear_kernel<__nv_bfloat16, __nv_bfloat16>;
-    return launch_k(kern, grid, kThreads, 0, a.stream, a);
+    return launch_k(linear_kernel<float, float>, grid, kThreads, 0, a.stream, a);
 }
 
 cudaError_t launch_linear_backward(const LinearBwdArgs& a) {
     cudaError_t err =
         launch_k(linear_dz_kernel, dim3((a.N / 8 + kThreads - 1) / kThreads, a.E), kThreads, 0,
                  a.stream, a);
-    if (err == cudaSuccess && a.dx)
-        err = launch_k(linear_dx_kernel, dim3(blocks(a.K), blocks(a.rows) + a.E), kThreads, 0,
-                       a.stream, a);
+    if (err == cudaSuccess && a.dx) {
+        LinearArgs g{};
+        g.x = a.dz;
+        g.offsets = a.offsets;
+        g.W = a.W;
+        g.rows = a.rows;
+        g.K = a.N;  // the reduction
+        g.N = a.K;
+        g.E = a.E;
+        g.dt = g.y_dt = MOE_BF16;
+        g.y = a.dx;
+        g.status = a.status;
+        g.counters = a.counters;
+        g.partials = a.partials;
+        g.stream = a.stream;
+        err = launch_linear_bf16(g, /*transposed=*/true);
+    }
     if (err == cudaSuccess && a.dW)
         err = launch_k(a.dw_dt == MOE_F32 ? linear_dw_kernel<float> : linear_dw_kernel<__nv_bfloat16>,
                        dim3(blocks(a.K), blocks(a.N), a.E), kThreads, 0, a.stream, a);

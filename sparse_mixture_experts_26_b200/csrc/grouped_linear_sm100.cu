@@ -1,0 +1,648 @@
+// grouped_linear_sm100.cu -- the grouped linear operators' products over the groups' rows
+// on the tensor cores:
+//   forward      out[r, f] = act(sum_c x[r, c] W_e[f, c] + b_e[f]) + residual[r, f]
+//   transposed   out[r, f] = sum_c x[r, c] W_e[c, f]          (the backward's dx = dz W_e)
+// for the rows r of each group e, with the pre-activation kept in 8 bits on request.
+//
+// The weights are the M operand and the tokens the N operand ("swapped"): a tile is 128
+// features (256 on a pair of SMs) x up to 256 tokens, and the tensor core's time goes with
+// the tokens' number in steps of 16 (32 on a pair), so a ragged group wastes less than one
+// such step where token rows on the M side would waste up to 127.  The tokens of a group
+// are cut into the fewest tiles of at most 256, all of nearly the same width.
+//
+// Layout: every CTA is persistent; warp 0 feeds a ring of TMA stages (64 of the reduction:
+// 128 features, 16 KiB, over the tile's token rows in boxes of 16 or 32), warp 1 issues
+// tcgen05.mma (fp32 accumulator in TMEM, two of 256 columns), warps 2-5 drain the other
+// accumulator.  The ring's stage size goes by the widest tile of this call, read from
+// `offsets` on the device: 11 stages for 16 tokens, 6 on a pair for 256.  Forward weights
+// are K-major; the transposed product reads the same weights MN-major (64 x 64 boxes).
+//
+// Epilogue: TMEM lanes are features and columns tokens, so 16 columns at a time go through
+// shared memory (one bank per lane) and come back with eight consecutive features of one
+// token per thread: bias, residual, activation and the output are 16-byte accesses, a row's
+// 128 features are written together, and a checkpoint block of 32 features is four
+// neighbouring lanes (two shuffles for its largest magnitude).
+//
+// Split reduction: tiles are dealt out round by round.  Where the last round would leave
+// SMs idle, its tiles are cut along the reduction instead (equal shares of all remaining
+// 64-steps, at most two tiles each): every share's fp32 tile goes to the workspace, and the
+// CTA that finishes a tile last adds the shares in the order of the reduction, whoever it
+// is, so the result does not depend on the timing; nobody waits for anybody.
+//
+// Every wait is bounded (sm100_ptx.cuh).
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "act_checkpoint.cuh"
+#include "moe_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace moe {
+
+// Defined in grouped_gemm_sm100.cu.
+bool encode_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                    uint32_t box_rows);
+bool encode_bf16_3d(CUtensorMap* map, const void* base, uint64_t batches, uint64_t rows,
+                    uint64_t cols, uint32_t box_rows);
+
+namespace {
+
+constexpr int kBK = 64;                // reduction per stage
+constexpr int kF = 128;                // features per CTA (TMEM lanes)
+constexpr int kTokens = 256;           // most token columns of a tile
+constexpr int kABytes = kF * kBK * 2;  // 16 KiB
+constexpr int kRingBytes = 204 * 1024;
+constexpr int kMaxStages = 11;
+constexpr int kThreads = 192;
+constexpr int kEpiThreads = 128;
+constexpr int kRound = 16;             // token columns per epilogue round
+constexpr int kPitch = kF + 4;         // staged token row, floats (16-byte rows)
+constexpr int kStagingBytes = 2 * kRound * kPitch * 4;
+constexpr int kBookBytes = 1024;
+constexpr int kSmemBytes = kRingBytes + kStagingBytes + kBookBytes + 1024 /*align*/;
+static_assert(kSmemBytes <= 232448, "shared memory");
+constexpr int kStageBarrier = 1;
+constexpr int kVoteBarrier = 2;
+constexpr uint16_t kBothCtas = 0x3;
+// A split is worth it from this many 64-steps saved per CTA (below, writing and joining
+// the shares costs more), and a share has at least kMinShare of them.
+constexpr int kMinSaved = 8;
+constexpr int kMinShare = 4;
+
+struct Args {
+    const int32_t* offsets;
+    int E, rows;
+    int F;                // output features
+    int C;                // reduction length
+    int box;              // token rows per TMA box
+    int group;            // token tiles whose rows stay in L2 together
+    int act;
+    const __nv_bfloat16* bias;
+    const __nv_bfloat16* residual;
+    void* out;
+    int out_f32;
+    int8_t* codes;
+    float* scales;
+    uint32_t* counters;
+    float* partials;
+    int slot_tokens;
+    uint32_t* status;
+};
+
+struct Book {
+    uint64_t full[kMaxStages];
+    uint64_t empty[kMaxStages];
+    uint64_t tmem_full[2];
+    uint64_t tmem_empty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    int last;                         // this CTA joins the tile's shares
+    int off[kMaxExperts + 1];
+    int tile_start[kMaxExperts + 1];
+    int stages, stage_bytes;
+    int one_tile_each;                // no group has a second token tile
+};
+static_assert(sizeof(Book) <= kBookBytes, "bookkeeping reserve");
+
+struct Tile {
+    int e, f0, row0, n, nt;  // n tokens from output row row0 on, nt columns (n rounded up)
+};
+
+// STEP: granularity of a tile's token columns.
+template <int STEP>
+__device__ __forceinline__ Tile decode_tile(const Book& bk, const Args& a, int ftiles, int fwidth,
+                                            int tile) {
+    int g = 0;
+    while (g + 1 < a.E && tile >= bk.tile_start[g + 1]) ++g;
+    const int local = tile - bk.tile_start[g];
+    const int n = bk.off[g + 1] - bk.off[g];
+    const int tt = (n + kTokens - 1) / kTokens;
+    // token tiles in runs of `group`; inside a run feature tiles are outer and token tiles
+    // inner, so that CTAs running together share the weights
+    const int per_full = a.group * ftiles;
+    const int run = local / per_full;
+    const int r = local - run * per_full;
+    const int left = tt - run * a.group;
+    const int width = left < a.group ? left : a.group;
+    const int i = run * a.group + r % width;
+    const int units = (n + STEP - 1) / STEP, base = units / tt, more = units - base * tt;
+    const int start = (i * base + (i < more ? i : more)) * STEP;
+    Tile t;
+    t.e = g;
+    t.f0 = (r / width) * fwidth;
+    t.row0 = bk.off[g] + start;
+    t.nt = (base + (i < more ? 1 : 0)) * STEP;
+    t.n = n - start < t.nt ? n - start : t.nt;
+    return t;
+}
+
+// The work of CTA (or pair) c of G: `rounds` whole tiles, then either one more whole tile
+// or a share of the remaining `rem` tiles' reduction.
+struct Plan {
+    int G, c, num_kb, rounds, rem, share_ctas;
+    __device__ __forceinline__ Plan(int G_, int c_, int total, int num_kb_)
+        : G(G_), c(c_), num_kb(num_kb_) {
+        rounds = total / G;
+        rem = total - rounds * G;
+        share_ctas = 0;
+        if (rem > 0) {
+            const long long units = static_cast<long long>(rem) * num_kb;
+            long long most = units / kMinShare;
+            if (most > G) most = G;
+            // steps saved on the busiest CTA by sharing the last round
+            if (most > rem && num_kb - (units + most - 1) / most >= kMinSaved)
+                share_ctas = static_cast<int>(most);
+        }
+    }
+    __device__ __forceinline__ long long bound(int i) const {  // first 64-step of share i
+        return static_cast<long long>(i) * rem * num_kb / share_ctas;
+    }
+    // Piece i of this CTA's work; false when there is none.
+    __device__ __forceinline__ bool get(int i, int& tile, int& kb0, int& kb1) const {
+        kb0 = 0;
+        kb1 = num_kb;
+        if (i < rounds) {
+            tile = i * G + c;
+            return true;
+        }
+        i -= rounds;
+        if (share_ctas == 0) {
+            tile = rounds * G + c;
+            return i == 0 && c < rem;
+        }
+        if (c >= share_ctas || i > 1) return false;
+        const long long u0 = bound(c), u1 = bound(c + 1);
+        const long long first = u0 / num_kb;
+        tile = rounds * G + static_cast<int>(first) + i;
+        const long long end = u1 - first * num_kb;  // relative to the first tile's start
+        if (i == 0) {
+            kb0 = static_cast<int>(u0 - first * num_kb);
+            kb1 = end < num_kb ? static_cast<int>(end) : num_kb;
+            return true;
+        }
+        kb1 = static_cast<int>(end - num_kb);
+        return kb1 > 0;
+    }
+    // Shares first .. last hold remaining tile t.
+    __device__ __forceinline__ int holder(long long u) const {
+        int i = static_cast<int>(u * share_ctas / (static_cast<long long>(rem) * num_kb));
+        while (i + 1 < share_ctas && bound(i + 1) <= u) ++i;
+        while (i > 0 && bound(i) > u) --i;
+        return i;
+    }
+};
+
+template <bool PAIR, bool TRANSPOSED>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_sm100_kernel(const __grid_constant__ CUtensorMap tmW,
+                        const __grid_constant__ CUtensorMap tmX, const Args args) {
+    constexpr int kCtas = PAIR ? 2 : 1;
+    constexpr int kStep = PAIR ? 32 : 16;
+    constexpr int kTileF = kF * kCtas;
+    constexpr uint32_t kTmemCols = 2 * kTokens;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    float* staging = reinterpret_cast<float*>(smem + kRingBytes);
+    Book& bk = *reinterpret_cast<Book*>(smem + kRingBytes + kStagingBytes);
+    volatile int* abort_flag = &bk.abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+    const int ftiles = (args.F + kTileF - 1) / kTileF;
+    const int num_kb = (args.C + kBK - 1) / kBK;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kMaxStages; ++s) {
+            mbar_init(&bk.full[s], 1);
+            mbar_init(&bk.empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&bk.tmem_full[a], 1);
+            mbar_init(&bk.tmem_empty[a], kCtas * kEpiThreads);
+        }
+        mbar_init(&bk.drain, 1);
+        bk.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+    }
+    if (warp == 1) {
+        if (PAIR)
+            tmem_alloc_pair(&bk.tmem_base, kTmemCols);
+        else
+            tmem_alloc(&bk.tmem_base, kTmemCols);
+    }
+    pdl_wait();
+    if (threadIdx.x == 0) {
+        load_group_bounds(args.offsets, args.E, args.rows, bk.off);
+        int widest = kStep, most = 0;
+        bk.tile_start[0] = 0;
+        for (int g = 0; g < args.E; ++g) {
+            const int n = bk.off[g + 1] - bk.off[g];
+            const int tt = (n + kTokens - 1) / kTokens;
+            bk.tile_start[g + 1] = bk.tile_start[g] + tt * ftiles;
+            if (tt > 0) {
+                const int units = (n + kStep - 1) / kStep;
+                const int w = (units + tt - 1) / tt * kStep;
+                widest = w > widest ? w : widest;
+                most = tt > most ? tt : most;
+            }
+        }
+        const int boxes = (widest / kCtas + args.box - 1) / args.box;
+        bk.stage_bytes = kABytes + boxes * args.box * kBK * 2;
+        const int fit = kRingBytes / bk.stage_bytes;
+        bk.stages = fit < kMaxStages ? fit : kMaxStages;
+        bk.one_tile_each = most <= 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (PAIR) cluster_sync();  // both CTAs' barriers exist before either signals the other
+    tc_fence_after();
+
+    const uint32_t tmem_base = bk.tmem_base;
+    const int stages = bk.stages, stage_bytes = bk.stage_bytes;
+    const Plan plan(gridDim.x / kCtas, blockIdx.x / kCtas, bk.tile_start[args.E], num_kb);
+    int tile, kb0, kb1;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, pending = 0, pending_phase = 0;
+            bool ok = true, issued = false;
+            // weights that no second token tile reads again leave L2 first
+            const bool stream = bk.one_tile_each != 0;
+            const uint64_t policy = l2_policy_evict_first();
+            for (int i = 0; ok && plan.get(i, tile, kb0, kb1); ++i) {
+                const Tile t = decode_tile<kStep>(bk, args, ftiles, kTileF, tile);
+                const int half = t.nt / kCtas;
+                const int boxes = (half + args.box - 1) / args.box;
+                const int x_row = t.row0 + static_cast<int>(rank) * half;
+                const int f = t.f0 + static_cast<int>(rank) * kF;
+                const uint32_t bytes =
+                    static_cast<uint32_t>(kABytes + boxes * args.box * kBK * 2);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait_bounded(&bk.empty[stage], phase ^ 1u, abort_flag,
+                                           args.status)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* w = smem + stage * stage_bytes;
+                    uint8_t* x = w + kABytes;
+                    const int c = kb * kBK;
+                    if (PAIR) {
+                        const uint32_t bar = map_to_cta(smem_u32(&bk.full[stage]), 0);
+                        if (leader) mbar_arrive_expect_tx(&bk.full[stage], 2 * bytes);
+                        if (TRANSPOSED) {
+                            tma_load_3d_pair(&tmW, bar, w, f, c, t.e);
+                            tma_load_3d_pair(&tmW, bar, w + kMnBoxBytes, f + 64, c, t.e);
+                        } else {
+                            tma_load_3d_pair(&tmW, bar, w, c, f, t.e);
+                        }
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d_pair(&tmX, bar, x + b * args.box * kBK * 2, c,
+                                             x_row + b * args.box);
+                    } else {
+                        uint64_t* bar = &bk.full[stage];
+                        mbar_arrive_expect_tx(bar, bytes);
+                        if (TRANSPOSED) {
+                            if (stream) {
+                                tma_load_3d_hint(&tmW, bar, w, f, c, t.e, policy);
+                                tma_load_3d_hint(&tmW, bar, w + kMnBoxBytes, f + 64, c, t.e,
+                                                 policy);
+                            } else {
+                                tma_load_3d(&tmW, bar, w, f, c, t.e);
+                                tma_load_3d(&tmW, bar, w + kMnBoxBytes, f + 64, c, t.e);
+                            }
+                        } else if (stream) {
+                            tma_load_3d_hint(&tmW, bar, w, c, f, t.e, policy);
+                        } else {
+                            tma_load_3d(&tmW, bar, w, c, f, t.e);
+                        }
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d(&tmX, bar, x + b * args.box * kBK * 2, c,
+                                        x_row + b * args.box);
+                    }
+                    issued = true;
+                    pending |= 1u << stage;
+                    pending_phase = (pending_phase & ~(1u << stage)) | (phase << stage);
+                    if (++stage == stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok && issued) {
+                if (leader) {
+                    for (int s = 0; s < stages; ++s)
+                        if (pending & (1u << s)) drain_wait(&bk.full[s], (pending_phase >> s) & 1u);
+                } else {
+                    // the peer's copies complete on the leader's barriers: time to land
+                    // before this CTA's shared memory can be released
+                    short_pause_ns(2000000ull);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (leader)
+        if (lane == 0 && leader) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true, issued = false;
+            for (int i = 0; ok && plan.get(i, tile, kb0, kb1); ++i) {
+                const Tile t = decode_tile<kStep>(bk, args, ftiles, kTileF, tile);
+                const uint32_t idesc = idesc_bf16_f32_major(kTileF, t.nt, TRANSPOSED, false);
+                if (!mbar_wait_bounded(&bk.tmem_empty[acc], acc_phase ^ 1u, abort_flag,
+                                       args.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kTokens);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait_bounded(&bk.full[stage], phase, abort_flag, args.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t w = smem_u32(smem + stage * stage_bytes);
+                    const uint64_t wd = TRANSPOSED ? sw128_mn_desc(w) : sw128_kmajor_desc(w);
+                    const uint64_t xd = sw128_kmajor_desc(w + kABytes);
+                    constexpr uint64_t kWStep = TRANSPOSED ? kMnDescStep : kKDescStep;
+#pragma unroll
+                    for (int k = 0; k < kBK / 16; ++k) {
+                        const uint32_t accumulate = (kb != kb0 || k != 0) ? 1u : 0u;
+                        if (PAIR)
+                            umma_bf16_pair(d_tmem, wd + kWStep * k, xd + kKDescStep * k, idesc,
+                                           accumulate);
+                        else
+                            umma_bf16(d_tmem, wd + kWStep * k, xd + kKDescStep * k, idesc,
+                                      accumulate);
+                    }
+                    if (PAIR)
+                        umma_commit_pair(&bk.empty[stage], kBothCtas);
+                    else
+                        umma_commit(&bk.empty[stage]);
+                    issued = true;
+                    if (++stage == stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (PAIR)
+                    umma_commit_pair(&bk.tmem_full[acc], kBothCtas);
+                else
+                    umma_commit(&bk.tmem_full[acc]);
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            if (!ok && issued) {
+                if (PAIR)
+                    umma_commit_pair(&bk.drain, 0x1);
+                else
+                    umma_commit(&bk.drain);
+                drain_wait(&bk.drain, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3;
+        const int et = static_cast<int>(threadIdx.x) - 64;  // 0 .. 127
+        const int my_tok = et >> 4;                         // token of a round: my_tok, + 8
+        const int j = et & 15;                              // features 8 j .. 8 j + 7
+        // Two 16-byte reads of the staged row cover eight features; swapping their order in
+        // every other group of four lanes keeps eight lanes on distinct banks.
+        const int swap = (j >> 2) & 1;
+        const int nb = ckpt_blocks(args.F);
+        const uint32_t free0 = PAIR ? map_to_cta(smem_u32(&bk.tmem_empty[0]), 0) : 0u;
+        const uint32_t free1 = PAIR ? map_to_cta(smem_u32(&bk.tmem_empty[1]), 0) : 0u;
+        auto release = [&](int acc) {
+            tc_fence_before();
+            if (PAIR)
+                mbar_arrive_cluster(acc == 0 ? free0 : free1);
+            else
+                mbar_arrive(&bk.tmem_empty[acc]);
+        };
+        auto sync_epilogue = [&]() {
+            asm volatile("bar.sync %0, %1;" ::"n"(kStageBarrier), "n"(kEpiThreads) : "memory");
+        };
+        const size_t slot_floats = static_cast<size_t>(kF) * args.slot_tokens;
+        int acc = 0, buf = 0;
+        uint32_t acc_phase = 0;
+        for (int i = 0; plan.get(i, tile, kb0, kb1); ++i) {
+            const Tile t = decode_tile<kStep>(bk, args, ftiles, kTileF, tile);
+            if (!bar_all(mbar_wait_bounded(&bk.tmem_full[acc], acc_phase, abort_flag, args.status),
+                         kVoteBarrier, kEpiThreads))
+                break;
+            tc_fence_after();
+            const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                   static_cast<uint32_t>(acc * kTokens);
+            const int f = t.f0 + static_cast<int>(rank) * kF + 8 * j;
+            const bool have_f = f < args.F;  // F is a multiple of 8: all eight or none
+            float bias[8] = {};
+            if (args.bias != nullptr && have_f)
+                load8(args.bias + static_cast<size_t>(t.e) * args.F + f, bias);
+            // the eight sums of token `tok` -> checkpoint, activation, residual, output
+            auto finish = [&](int tok, float (&v)[8]) {
+                const bool valid = have_f && tok < t.n;
+                const size_t row = static_cast<size_t>(t.row0 + tok);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] += bias[k];
+                if (args.codes != nullptr) {
+                    uint32_t mag = 0;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) mag = max(mag, ckpt_mag(v[k]));
+                    if (!have_f) mag = 0;
+                    mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+                    mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+                    const float s = ckpt_scale(mag);
+                    if (valid) {
+                        *reinterpret_cast<uint2*>(args.codes + row * args.F + f) =
+                            ckpt_pack8(v, s);
+                        if ((j & 3) == 0) args.scales[row * nb + f / kCkptBlock] = s;
+                    }
+                }
+                if (!valid) return;
+                if (args.act != MOE_ACT_NONE) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = act_value(args.act, v[k]);
+                }
+                if (args.residual != nullptr) {
+                    float r[8];
+                    load8(args.residual + row * args.F + f, r);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] += r[k];
+                }
+                if (args.out_f32)
+                    store8(static_cast<float*>(args.out) + row * args.F + f, v);
+                else
+                    store8(static_cast<__nv_bfloat16*>(args.out) + row * args.F + f, v);
+            };
+
+            if (kb1 - kb0 == num_kb) {
+                for (int c0 = 0; c0 < t.nt; c0 += kRound) {
+                    uint32_t r[kRound];
+                    tmem_ld_16cols(tbase + c0, r);
+                    tmem_ld_wait();
+                    if (c0 + kRound >= t.nt) release(acc);
+                    float* st = staging + buf * kRound * kPitch;
+#pragma unroll
+                    for (int k = 0; k < kRound; ++k) st[k * kPitch + q * 32 + lane] = bits_f32(r[k]);
+                    sync_epilogue();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int tok = my_tok + 8 * h;
+                        const float4* src =
+                            reinterpret_cast<const float4*>(st + tok * kPitch + 8 * j);
+                        const float4 p = src[swap], s = src[swap ^ 1];
+                        const float4 lo = swap ? s : p, hi = swap ? p : s;
+                        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                        finish(c0 + tok, v);
+                    }
+                    buf ^= 1;
+                }
+            } else {
+                // a share: the fp32 tile to the workspace as [token][feature]
+                const int seg = i - plan.rounds;
+                const int rem_tile = tile - plan.rounds * plan.G;
+                float* slot = args.partials +
+                              static_cast<size_t>((plan.c * 2 + seg) * kCtas + rank) * slot_floats;
+                for (int c0 = 0; c0 < t.nt; c0 += kRound) {
+                    uint32_t r[kRound];
+                    tmem_ld_16cols(tbase + c0, r);
+                    tmem_ld_wait();
+                    if (c0 + kRound >= t.nt) release(acc);
+#pragma unroll
+                    for (int k = 0; k < kRound; ++k)
+                        __stcg(slot + (c0 + k) * kF + q * 32 + lane, bits_f32(r[k]));
+                }
+                const long long u = static_cast<long long>(rem_tile) * num_kb;
+                const int first = plan.holder(u), last = plan.holder(u + num_kb - 1);
+                uint32_t* counter = args.counters + rem_tile * kCtas + rank;
+                __threadfence();
+                sync_epilogue();
+                if (et == 0) {
+                    const uint32_t before = atomicAdd(counter, 1u);
+                    bk.last = before == static_cast<uint32_t>(last - first);
+                    if (bk.last) *counter = 0;  // zero again for the next call
+                }
+                sync_epilogue();
+                if (bk.last) {
+                    __threadfence();
+                    for (int tok = my_tok; tok < t.nt; tok += 8) {
+                        float v[8] = {};
+                        for (int s = first; s <= last; ++s) {
+                            const int sseg = plan.bound(s) / num_kb == rem_tile ? 0 : 1;
+                            const float4* src = reinterpret_cast<const float4*>(
+                                args.partials +
+                                static_cast<size_t>((s * 2 + sseg) * kCtas + rank) * slot_floats +
+                                tok * kF + 8 * j);
+                            const float4 lo = __ldcg(src), hi = __ldcg(src + 1);
+                            v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
+                            v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
+                        }
+                        finish(tok, v);
+                    }
+                }
+            }
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (PAIR) cluster_sync();  // the leader's MMAs into this CTA's TMEM are done
+    if (warp == 1) {
+        tc_fence_after();
+        if (PAIR)
+            tmem_dealloc_pair(tmem_base, kTmemCols);
+        else
+            tmem_dealloc(tmem_base, kTmemCols);
+    }
+}
+
+template <bool PAIR, bool TRANSPOSED>
+cudaError_t launch_engine(const LinearArgs& a, int F, int C) {
+    constexpr int kCtas = PAIR ? 2 : 1;
+    auto kern = linear_sm100_kernel<PAIR, TRANSPOSED>;
+    static PerDeviceOnce once;
+    if (const cudaError_t err = opt_in_smem(once, kern, kSmemBytes); err != cudaSuccess) return err;
+    Args g{};
+    g.offsets = a.offsets;
+    g.E = a.E;
+    g.rows = a.rows;
+    g.F = F;
+    g.C = C;
+    g.box = a.rows <= kTokens ? 16 : 32;
+    // token rows of a run: at most about 64 MB, half of L2
+    const long long tile_bytes = static_cast<long long>(kTokens) * C * 2;
+    const long long run = (64LL << 20) / tile_bytes;
+    g.group = static_cast<int>(run < 1 ? 1 : (run > 1024 ? 1024 : run));
+    g.act = a.act;
+    g.bias = static_cast<const __nv_bfloat16*>(a.bias);
+    g.residual = static_cast<const __nv_bfloat16*>(a.residual);
+    g.out = a.y;
+    g.out_f32 = a.y_dt == MOE_F32;
+    g.codes = a.codes;
+    g.scales = a.scales;
+    g.counters = a.counters;
+    g.partials = a.partials;
+    g.slot_tokens = linear_slot_tokens(a.rows);
+    g.status = a.status;
+    CUtensorMap w, x;
+    if (!(TRANSPOSED ? encode_bf16_3d(&w, a.W, a.E, C, F, 64) : encode_bf16_3d(&w, a.W, a.E, F, C, kF)) ||
+        !encode_bf16_2d(&x, a.x, a.rows, C, g.box))
+        return cudaErrorInvalidValue;
+    int sms = device_sm_count();
+    if (sms > kLinearMaxCtas) sms = kLinearMaxCtas;
+    // Most tiles there can be: the groups' token tiles, each with its feature tiles.  A
+    // reduction long enough to be shared can use every SM.
+    const long long ftiles = (F + kF * kCtas - 1) / (kF * kCtas);
+    const long long groups = a.rows < a.E ? a.rows : a.E;
+    const long long tiles = (a.rows / kTokens + groups) * ftiles;
+    const long long shares = (C + kBK - 1) / kBK / kMinShare;
+    const long long want = tiles * (shares < 1 ? 1 : shares);
+    const int units = static_cast<int>(want < sms / kCtas ? want : sms / kCtas);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(units * kCtas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[1];
+    if (PAIR) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, w, x, g);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+// Average rows per group from which the products run on pairs of SMs.
+constexpr int kPairRowsPerGroup = 256;
+
+}  // namespace
+
+cudaError_t launch_linear_bf16(const LinearArgs& a, bool transposed) {
+    const int F = a.N, C = a.K;
+    if (a.rows / a.E >= kPairRowsPerGroup && pair_gemm_enabled()) {
+        const cudaError_t err =
+            transposed ? launch_engine<true, true>(a, F, C) : launch_engine<true, false>(a, F, C);
+        if (err == cudaSuccess || err == cudaErrorInvalidValue) return err;
+        cudaGetLastError();  // no room for a pair of CTAs: single SMs
+    }
+    return transposed ? launch_engine<false, true>(a, F, C) : launch_engine<false, false>(a, F, C);
+}
+
+}  // namespace moe

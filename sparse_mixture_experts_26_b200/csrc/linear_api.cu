@@ -22,6 +22,8 @@ moe_status check_linear(int rows, int K, int N, int E, moe_dtype dt) {
     // offsets are 64-bit
     if (static_cast<long long>(E) * N >= (1LL << 31) || static_cast<long long>(E) * K >= (1LL << 31))
         return MOE_ERR_UNSUPPORTED;
+    const long long widest = K > N ? K : N;
+    if (rows * widest >= (1LL << 40)) return MOE_ERR_UNSUPPORTED;  // tile counts in 32 bits
     return MOE_OK;
 }
 
@@ -31,9 +33,9 @@ bool optional_ok(const void* p) { return aligned16(p); }  // null is aligned
 
 // Workspace regions (1 KiB aligned): status word, counters.
 struct LinearWs {
-    size_t status, dz, total;
+    size_t status, counters, partials, dz, total;
 };
-LinearWs linear_ws(int rows, int N, bool backward) {
+LinearWs linear_ws(int rows, int N, moe_dtype dt, bool backward) {
     LinearWs L{};
     size_t o = 0;
     auto take = [&](size_t bytes) {
@@ -42,6 +44,8 @@ LinearWs linear_ws(int rows, int N, bool backward) {
         return at;
     };
     L.status = take(256);
+    L.counters = take(kLinearCounters * 4);
+    L.partials = take(dt == MOE_BF16 ? linear_partial_floats(rows) * 4 : 0);
     L.dz = take(backward ? static_cast<size_t>(rows) * N * 2 : 0);
     L.total = o;
     return L;
@@ -84,7 +88,7 @@ moe_status linear_impl(const char* name, bool train, const void* x, const int32_
         !optional_ok(offsets) || (offsets == nullptr && E != 1))
         return MOE_ERR_INVALID_ARG;
     if (train && !ptrs_ok({codes, scales})) return MOE_ERR_INVALID_ARG;
-    const LinearWs L = linear_ws(rows, N, false);
+    const LinearWs L = linear_ws(rows, N, dt, false);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
     Range range(name);
     LinearArgs a{};
@@ -104,6 +108,8 @@ moe_status linear_impl(const char* name, bool train, const void* x, const int32_
     a.codes = codes;
     a.scales = scales;
     a.status = at<uint32_t>(ws, L.status);
+    a.counters = at<uint32_t>(ws, L.counters);
+    a.partials = at<float>(ws, L.partials);
     a.stream = stream;
     return finish_linear(launch_linear(a), stream, a.status);
 }
@@ -117,7 +123,7 @@ extern "C" {
 
 size_t moe_grouped_linear_workspace_bytes(int rows, int K, int N, int E, moe_dtype dt) {
     if (check_linear(rows, K, N, E, dt) != MOE_OK) return 0;
-    return linear_ws(rows, N, false).total;
+    return linear_ws(rows, N, dt, false).total;
 }
 
 moe_status moe_grouped_linear(const void* x, const int32_t* offsets, const void* W,
@@ -161,7 +167,7 @@ moe_status moe_checkpoint_restore(const int8_t* codes, const float* scales, int 
 
 size_t moe_grouped_linear_backward_workspace_bytes(int rows, int K, int N, int E, moe_dtype dt) {
     if (check_linear(rows, K, N, E, dt) != MOE_OK || dt != MOE_BF16) return 0;
-    return linear_ws(rows, N, true).total;
+    return linear_ws(rows, N, dt, true).total;
 }
 
 moe_status moe_grouped_linear_backward(const void* dy, const void* x, const int32_t* offsets,
@@ -186,7 +192,7 @@ moe_status moe_grouped_linear_backward(const void* dy, const void* x, const int3
     }
     if (!ptrs_ok({dy, x, W, ws})) return MOE_ERR_INVALID_ARG;
     if (act != MOE_ACT_NONE && !ptrs_ok({codes, scales})) return MOE_ERR_INVALID_ARG;
-    const LinearWs L = linear_ws(rows, N, true);
+    const LinearWs L = linear_ws(rows, N, dt, true);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
     Range range("moe_grouped_linear_backward");
     LinearBwdArgs a{};
@@ -207,6 +213,8 @@ moe_status moe_grouped_linear_backward(const void* dy, const void* x, const int3
     a.db = db;
     a.dz = at<void>(ws, L.dz);
     a.status = at<uint32_t>(ws, L.status);
+    a.counters = at<uint32_t>(ws, L.counters);
+    a.partials = at<float>(ws, L.partials);
     a.stream = stream;
     return finish_linear(launch_linear_backward(a), stream, a.status);
 }

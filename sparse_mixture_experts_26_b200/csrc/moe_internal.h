@@ -306,8 +306,20 @@ struct LinearArgs {
     int8_t* codes;           // or nullptr
     float* scales;
     uint32_t* status;
+    uint32_t* counters;      // kLinearCounters words, zero between calls
+    float* partials;         // linear_partial_floats(rows)
     cudaStream_t stream;
 };
+// Blocks of one launch, and with them the partial tiles in the workspace, are limited to
+// this (a B200 has 148 SMs): the layout must not depend on the device.
+constexpr int kLinearMaxCtas = 160;
+constexpr int kLinearCounters = kLinearMaxCtas;
+// Token columns of the widest tile that `rows` rows can give, and the fp32 values of two
+// partial tiles (128 features each) per block.
+inline int linear_slot_tokens(int rows) { return rows >= 256 ? 256 : (rows + 31) / 32 * 32; }
+inline size_t linear_partial_floats(int rows) {
+    return static_cast<size_t>(kLinearMaxCtas) * 2 * 128 * linear_slot_tokens(rows);
+}
 cudaError_t launch_linear(const LinearArgs& a);
 
 // Backward; W [E, N, K] as in the forward.
@@ -326,9 +338,14 @@ struct LinearBwdArgs {
     float* db;               // or nullptr
     void* dz;                // bf16 [rows, N] scratch
     uint32_t* status;
+    uint32_t* counters;
+    float* partials;
     cudaStream_t stream;
 };
 cudaError_t launch_linear_backward(const LinearBwdArgs& a);
+// The bf16 products over the groups' rows on tensor cores: the forward, and with
+// transposed = true out[r, :] = x[r, :] W_e (W [E, K, N]: the backward's dx).
+cudaError_t launch_linear_bf16(const LinearArgs& a, bool transposed);
 cudaError_t launch_checkpoint_save(const void* v, int rows, int N, moe_dtype dt, int8_t* codes,
                                    float* scales, cudaStream_t s);
 cudaError_t launch_checkpoint_restore(const int8_t* codes, const float* scales, int rows, int N,

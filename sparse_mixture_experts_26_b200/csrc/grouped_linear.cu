@@ -132,62 +132,6 @@ __global__ void __launch_bounds__(kThreads) linear_kernel(const LinearArgs a) {
     }
 }
 
-// dz = dy act'(value of the code), and db = sum of dz over the group's rows, fp32.
-__global__ void __launch_bounds__(kThreads) linear_dz_kernel(const LinearBwdArgs a) {
-    __shared__ int off[kMaxExperts + 1];
-    if (threadIdx.x == 0) load_group_bounds(a.offsets, a.E, a.rows, off);
-    __syncthreads();
-    const int e = blockIdx.y, n = (blockIdx.x * kThreads + threadIdx.x) * 8;
-    if (n >= a.N) return;
-    const int nb = ckpt_blocks(a.N);
-    float sum[8] = {};
-    for (int r = off[e]; r < off[e + 1]; ++r) {
-        const size_t at = static_cast<size_t>(r) * a.N + n;
-        float g[8];
-        load8(static_cast<const __nv_bfloat16*>(a.dy) + at, g);
-        if (a.codes) {
-            float z[8];
-            ckpt_unpack8(*reinterpret_cast<const uint2*>(a.codes + at),
-                         a.scales[static_cast<size_t>(r) * nb + n / kCkptBlock], z);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) g[k] *= act_slope(a.act, z[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum[k] += g[k];
-        store8(static_cast<__nv_bfloat16*>(a.dz) + at, g);
-    }
-    if (a.db) store8(a.db + static_cast<size_t>(e) * a.N + n, sum);
-}
-
-template <typename TW>
-__global__ void __launch_bounds__(kThreads) linear_dw_kernel(const LinearBwdArgs a) {
-    __shared__ int off[kMaxExperts + 1];
-    if (threadIdx.x == 0) load_group_bounds(a.offsets, a.E, a.rows, off);
-    __syncthreads();
-    const int e = blockIdx.z, n0 = blockIdx.y * kT, k0 = blockIdx.x * kT;
-    const int r0 = off[e];
-    const auto* dz = static_cast<const __nv_bfloat16*>(a.dz);
-    const auto* x = static_cast<const __nv_bfloat16*>(a.x);
-    float acc[4][4] = {};
-    tile_product(
-        off[e + 1] - r0,
-        [&](int n, int c) {
-            return n0 + n < a.N ? to_f32(dz[static_cast<size_t>(r0 + c) * a.N + n0 + n]) : 0.f;
-        },
-        [&](int k, int c) {
-            return k0 + k < a.K ? to_f32(x[static_cast<size_t>(r0 + c) * a.K + k0 + k]) : 0.f;
-        },
-        acc);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + ty * 4 + i, k = k0 + tx + 16 * j;
-            if (n < a.N && k < a.K)
-                static_cast<TW*>(a.dW)[(static_cast<size_t>(e) * a.N + n) * a.K + k] =
-                    static_cast<TW>(acc[i][j]);
-        }
-}
-
 unsigned blocks(int n) { return static_cast<unsigned>((n + kT - 1) / kT); }
 
 }  // namespace
@@ -199,12 +143,10 @@ cudaError_t launch_linear(const LinearArgs& a) {
 }
 
 cudaError_t launch_linear_backward(const LinearBwdArgs& a) {
-    cudaError_t err =
-        launch_k(linear_dz_kernel, dim3((a.N / 8 + kThreads - 1) / kThreads, a.E), kThreads, 0,
-                 a.stream, a);
+    cudaError_t err = launch_linear_dz(a);
     if (err == cudaSuccess && a.dx) {
         LinearArgs g{};
-        g.x = a.dz;
+        g.x = a.codes ? a.dz : a.dy;
         g.offsets = a.offsets;
         g.W = a.W;
         g.rows = a.rows;
@@ -219,9 +161,7 @@ cudaError_t launch_linear_backward(const LinearBwdArgs& a) {
         g.stream = a.stream;
         err = launch_linear_bf16(g, /*transposed=*/true);
     }
-    if (err == cudaSuccess && a.dW)
-        err = launch_k(a.dw_dt == MOE_F32 ? linear_dw_kernel<float> : linear_dw_kernel<__nv_bfloat16>,
-                       dim3(blocks(a.K), blocks(a.N), a.E), kThreads, 0, a.stream, a);
+    if (err == cudaSuccess && a.dW) err = launch_linear_wgrad(a);
     return err;
 }
 

@@ -1,0 +1,436 @@
+// grouped_linear_wgrad_sm100.cu -- the grouped linear operators' weight gradient on the
+// tensor cores:
+//   dW[e, n, k] = sum over the rows r of group e of dz[r, n] x[r, k]
+// Both operands are rows as they lie in memory (n and k contiguous), read as MN-major
+// 64 x 64 boxes; nothing is transposed.  A tile is 128 features n (256 on a pair of SMs,
+// 128 from each) x 256 inputs k, the reduction runs over the group's rows in blocks of 64.
+//
+// A group starts and ends anywhere.  Its whole blocks come straight from dz and x; the rest
+// comes from the tail buffers (linear_rows.cu), where the group's last rows are followed
+// by zeros up to a multiple of 16, and only that many 16-row steps are issued.  So no row
+// outside the group is ever multiplied, not even by zero, and small groups (decode batches)
+// load a quarter of a stage.
+//
+// Bound: many rows, the tensor cores (pairs of SMs halve the bytes staged per product);
+// few rows, the gradient's own bytes (E N K elements written once).  The epilogue stages 32
+// rows x 128 bytes per warp and stores them by TMA (rows and columns past the matrix are
+// outside the tensor), with an L2 evict-first hint, since nobody reads them here again.  For
+// few rows the shared memory goes to staging buffers (2 stages, 8 buffers a warp) instead of
+// input stages (4 and 2; pairs 6 and 2).
+//
+// Roles, accumulators and bounded waits as in grouped_linear_sm100.cu.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "act_checkpoint.cuh"
+#include "moe_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace moe {
+
+// Defined in grouped_gemm_sm100.cu.
+bool encode_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                    uint32_t box_rows);
+bool encode_bf16_3d(CUtensorMap* map, const void* base, uint64_t batches, uint64_t rows,
+                    uint64_t cols, uint32_t box_rows);
+bool encode_f32_3d(CUtensorMap* map, const void* base, uint64_t batches, uint64_t rows,
+                   uint64_t cols, uint32_t box_cols, uint32_t box_rows);
+
+namespace {
+
+constexpr int kM = 128;              // features per CTA (TMEM lanes)
+constexpr int kN = 256;              // inputs per tile
+constexpr int kRows = kTailRows;     // reduction per stage
+constexpr int kBox = kMnBoxBytes;    // 64 columns x 64 rows
+constexpr int kSlab = 16 * 128;      // 64 columns x 16 rows
+constexpr int kThreads = 192;
+constexpr int kEpiThreads = 128;
+constexpr int kChunk = 32 * 128;     // staged output: 32 rows x 128 bytes
+constexpr int kVoteBarrier = 2;
+constexpr uint16_t kBothCtas = 0x3;
+
+struct Args {
+    const int32_t* offsets;
+    int E, rows;
+    int M;         // features (dz columns)
+    int N;         // inputs (x columns)
+    int m_tiles, n_tiles;
+    uint32_t* status;
+};
+
+template <int STAGES>
+struct Book {
+    uint64_t full[STAGES];
+    uint64_t empty[STAGES];
+    uint64_t tmem_full[2];
+    uint64_t tmem_empty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    int off[kMaxExperts + 1];
+};
+
+template <bool PAIR, int STAGES, int BUFS>
+struct Shape {
+    static constexpr int kABytes = 2 * kBox;
+    static constexpr int kBBoxes = PAIR ? 2 : 4;  // a pair's CTAs hold half of x's columns
+    static constexpr int kStageBytes = kABytes + kBBoxes * kBox;
+    static constexpr int kStaging = 4 * BUFS * kChunk;
+    static constexpr int kSmem = STAGES * kStageBytes + kStaging + 1024 /*book*/ + 1024 /*align*/;
+    static_assert(kSmem <= 232448, "shared memory");
+    static_assert(sizeof(Book<STAGES>) <= 1024, "bookkeeping reserve");
+};
+
+template <bool PAIR, bool F32, int STAGES, int BUFS>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_wgrad_kernel(const __grid_constant__ CUtensorMap tmZ,
+                        const __grid_constant__ CUtensorMap tmX,
+                        const __grid_constant__ CUtensorMap tmZt,
+                        const __grid_constant__ CUtensorMap tmXt,
+                        const __grid_constant__ CUtensorMap tmO, const Args args) {
+    using S = Shape<PAIR, STAGES, BUFS>;
+    constexpr int kCtas = PAIR ? 2 : 1;
+    constexpr uint32_t kIdesc = idesc_bf16_f32_major(kM * kCtas, kN, true, true);
+    constexpr uint32_t kTmemCols = 2 * kN;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* staging = smem + STAGES * S::kStageBytes;
+    auto& bk = *reinterpret_cast<Book<STAGES>*>(staging + S::kStaging);
+    volatile int* abort_flag = &bk.abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+    const bool leader = rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&bk.full[s], 1);
+            mbar_init(&bk.empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&bk.tmem_full[a], 1);
+            mbar_init(&bk.tmem_empty[a], kCtas * kEpiThreads);
+        }
+        mbar_init(&bk.drain, 1);
+        bk.abort_flag = 0;
+        fence_mbar_init();
+        load_group_bounds(args.offsets, args.E, args.rows, bk.off);
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmZ);
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmZt);
+        tma_prefetch_desc(&tmXt);
+        tma_prefetch_desc(&tmO);
+    }
+    if (warp == 1) {
+        if (PAIR)
+            tmem_alloc_pair(&bk.tmem_base, kTmemCols);
+        else
+            tmem_alloc(&bk.tmem_base, kTmemCols);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (PAIR) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = bk.tmem_base;
+    const int per_e = args.m_tiles * args.n_tiles;
+    const int total = args.E * per_e;
+    const int first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
+    // column tiles innermost: CTAs running together write neighbouring parts of the same
+    // gradient rows
+    auto tile_of = [&](int tile, int& e, int& m0, int& n0, int& row0, int& n) {
+        e = tile / per_e;
+        const int local = tile - e * per_e;
+        m0 = local / args.n_tiles * (kM * kCtas);
+        n0 = local % args.n_tiles * kN;
+        row0 = bk.off[e];
+        n = bk.off[e + 1] - row0;
+    };
+    int e, m0, n0, row0, n;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, pending = 0, pending_phase = 0;
+            bool ok = true, issued = false;
+            for (int tile = first; ok && tile < total; tile += step) {
+                tile_of(tile, e, m0, n0, row0, n);
+                const int mc = m0 + rank * kM;
+                const int nc = n0 + rank * (S::kBBoxes * 64);
+                for (int r = 0; r < n; r += kRows) {
+                    if (!mbar_wait_bounded(&bk.empty[stage], phase ^ 1u, abort_flag,
+                                           args.status)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* z = smem + stage * S::kStageBytes;
+                    uint8_t* x = z + S::kABytes;
+                    const bool whole = n - r >= kRows;
+                    const int slabs = whole ? 1 : (n - r + 15) / 16;
+                    const uint32_t bytes =
+                        static_cast<uint32_t>((2 + S::kBBoxes) * (whole ? kBox : slabs * kSlab));
+                    auto load = [&](const CUtensorMap* map, uint8_t* dst, int c, int row) {
+                        if (PAIR)
+                            tma_load_2d_pair(map, map_to_cta(smem_u32(&bk.full[stage]), 0), dst, c,
+                                             row);
+                        else
+                            tma_load_2d(map, &bk.full[stage], dst, c, row);
+                    };
+                    if (leader) mbar_arrive_expect_tx(&bk.full[stage], kCtas * bytes);
+                    if (whole) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+                            load(&tmZ, z + b * kBox, mc + 64 * b, row0 + r);
+#pragma unroll
+                        for (int b = 0; b < S::kBBoxes; ++b)
+                            load(&tmX, x + b * kBox, nc + 64 * b, row0 + r);
+                    } else {
+                        for (int s = 0; s < slabs; ++s) {
+                            const int row = e * kTailRows + 16 * s;
+                            for (int b = 0; b < 2; ++b)
+                                load(&tmZt, z + b * kBox + s * kSlab, mc + 64 * b, row);
+                            for (int b = 0; b < S::kBBoxes; ++b)
+                                load(&tmXt, x + b * kBox + s * kSlab, nc + 64 * b, row);
+                        }
+                    }
+                    issued = true;
+                    pending |= 1u << stage;
+                    pending_phase = (pending_phase & ~(1u << stage)) | (phase << stage);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok && issued) {
+                if (leader) {
+                    for (int s = 0; s < STAGES; ++s)
+                        if (pending & (1u << s)) drain_wait(&bk.full[s], (pending_phase >> s) & 1u);
+                } else {
+                    short_pause_ns(2000000ull);  // its copies complete on the leader's barriers
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true, issued = false;
+            for (int tile = first; ok && tile < total; tile += step) {
+                tile_of(tile, e, m0, n0, row0, n);
+                if (n == 0) continue;  // zeros, written by the epilogue alone
+                if (!mbar_wait_bounded(&bk.tmem_empty[acc], acc_phase ^ 1u, abort_flag,
+                                       args.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kN);
+                for (int r = 0; r < n; r += kRows) {
+                    if (!mbar_wait_bounded(&bk.full[stage], phase, abort_flag, args.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t z = smem_u32(smem + stage * S::kStageBytes);
+                    const uint64_t zd = sw128_mn_desc(z), xd = sw128_mn_desc(z + S::kABytes);
+                    const int left = n - r;
+                    const int steps = left >= kRows ? kRows / 16 : (left + 15) / 16;
+                    for (int k = 0; k < steps; ++k) {
+                        const uint32_t accumulate = (r != 0 || k != 0) ? 1u : 0u;
+                        if (PAIR)
+                            umma_bf16_pair(d_tmem, zd + kMnDescStep * k, xd + kMnDescStep * k,
+                                           kIdesc, accumulate);
+                        else
+                            umma_bf16(d_tmem, zd + kMnDescStep * k, xd + kMnDescStep * k, kIdesc,
+                                      accumulate);
+                    }
+                    if (PAIR)
+                        umma_commit_pair(&bk.empty[stage], kBothCtas);
+                    else
+                        umma_commit(&bk.empty[stage]);
+                    issued = true;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (PAIR)
+                    umma_commit_pair(&bk.tmem_full[acc], kBothCtas);
+                else
+                    umma_commit(&bk.tmem_full[acc]);
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            if (!ok && issued) {
+                if (PAIR)
+                    umma_commit_pair(&bk.drain, 0x1);
+                else
+                    umma_commit(&bk.drain);
+                drain_wait(&bk.drain, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        const int q = warp & 3;
+        uint8_t* wstage = staging + q * BUFS * kChunk;
+        const uint64_t policy = l2_policy_evict_first();
+        const uint32_t free0 = PAIR ? map_to_cta(smem_u32(&bk.tmem_empty[0]), 0) : 0u;
+        const uint32_t free1 = PAIR ? map_to_cta(smem_u32(&bk.tmem_empty[1]), 0) : 0u;
+        int acc = 0, buf = 0;
+        uint32_t acc_phase = 0;
+        for (int tile = first; tile < total; tile += step) {
+            tile_of(tile, e, m0, n0, row0, n);
+            if (n > 0) {
+                if (!bar_all(mbar_wait_bounded(&bk.tmem_full[acc], acc_phase, abort_flag,
+                                               args.status),
+                             kVoteBarrier, kEpiThreads))
+                    break;
+                tc_fence_after();
+            }
+            const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                   static_cast<uint32_t>(acc * kN);
+            const int mrow = m0 + rank * kM + q * 32;
+            constexpr int kCols = F32 ? 32 : 64;  // output columns per 128-byte chunk
+#pragma unroll 1
+            for (int c = 0; c < kN; c += kCols) {
+                uint4 out[8];  // this lane's row of the chunk
+                if (n == 0) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) out[i] = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                    uint32_t v[32];
+                    tmem_ld_32cols(tbase + c, v);
+                    if constexpr (F32) {
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            out[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    } else {
+                        uint32_t w[32];
+                        tmem_ld_32cols(tbase + c + 32, w);
+                        tmem_ld_wait();
+                        auto pack = [](const uint32_t* p) {
+                            return pack_bf16x2(bits_f32(p[0]), bits_f32(p[1]));
+                        };
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            out[i] = make_uint4(pack(v + 8 * i), pack(v + 8 * i + 2),
+                                                pack(v + 8 * i + 4), pack(v + 8 * i + 6));
+                            out[4 + i] = make_uint4(pack(w + 8 * i), pack(w + 8 * i + 2),
+                                                    pack(w + 8 * i + 4), pack(w + 8 * i + 6));
+                        }
+                    }
+                }
+                if (n0 + c >= args.N || mrow >= args.M) continue;  // uniform in the warp
+                uint8_t* st = wstage + buf * kChunk;
+                if (lane == 0) bulk_wait_group_read<BUFS - 1>();  // this buffer has been read
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4*>(st + lane * 128 + ((i ^ (lane & 7)) << 4)) = out[i];
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d_hint(&tmO, st, n0 + c, mrow, e, policy);
+                    bulk_commit_group();
+                }
+                if (++buf == BUFS) buf = 0;
+            }
+            if (n == 0) continue;
+            tc_fence_before();
+            if (PAIR)
+                mbar_arrive_cluster(acc == 0 ? free0 : free1);
+            else
+                mbar_arrive(&bk.tmem_empty[acc]);
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+        if (lane == 0) bulk_wait_group<0>();  // every store complete before the block exits
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (PAIR) cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        if (PAIR)
+            tmem_dealloc_pair(tmem_base, kTmemCols);
+        else
+            tmem_dealloc(tmem_base, kTmemCols);
+    }
+}
+
+template <bool PAIR, bool F32, int STAGES, int BUFS>
+cudaError_t launch_wgrad(const LinearBwdArgs& a) {
+    constexpr int kCtas = PAIR ? 2 : 1;
+    constexpr int kSmem = Shape<PAIR, STAGES, BUFS>::kSmem;
+    auto kern = linear_wgrad_kernel<PAIR, F32, STAGES, BUFS>;
+    static PerDeviceOnce once;
+    if (const cudaError_t err = opt_in_smem(once, kern, kSmem); err != cudaSuccess) return err;
+    const void* dz = a.codes ? a.dz : a.dy;
+    const uint64_t tails = static_cast<uint64_t>(a.E) * kTailRows;
+    CUtensorMap z, x, zt, xt, o;
+    if (!encode_bf16_2d(&z, dz, a.rows, a.N, kRows) || !encode_bf16_2d(&x, a.x, a.rows, a.K, kRows) ||
+        !encode_bf16_2d(&zt, a.dz_tail, tails, a.N, 16) ||
+        !encode_bf16_2d(&xt, a.x_tail, tails, a.K, 16) ||
+        !(F32 ? encode_f32_3d(&o, a.dW, a.E, a.N, a.K, 32, 32)
+              : encode_bf16_3d(&o, a.dW, a.E, a.N, a.K, 32)))
+        return cudaErrorInvalidValue;
+    Args g{};
+    g.offsets = a.offsets;
+    g.E = a.E;
+    g.rows = a.rows;
+    g.M = a.N;
+    g.N = a.K;
+    g.m_tiles = (a.N + kM * kCtas - 1) / (kM * kCtas);
+    g.n_tiles = (a.K + kN - 1) / kN;
+    g.status = a.status;
+    const long long tiles = static_cast<long long>(a.E) * g.m_tiles * g.n_tiles;
+    const int most = device_sm_count() / kCtas;
+    const int units = static_cast<int>(tiles < most ? tiles : most);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(units * kCtas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[1];
+    if (PAIR) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, z, x, zt, xt, o, g);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+// Average rows per group from which a pair of SMs shares a tile, and up to which the
+// output's bytes are the cost.
+constexpr int kPairRowsPerGroup = 256;
+constexpr int kShortRowsPerGroup = 64;
+
+template <bool F32>
+cudaError_t launch_typed(const LinearBwdArgs& a) {
+    const int mean = a.rows / a.E;
+    if (mean <= kShortRowsPerGroup) return launch_wgrad<false, F32, 2, 8>(a);
+    if (mean >= kPairRowsPerGroup && pair_gemm_enabled()) {
+        const cudaError_t err = launch_wgrad<true, F32, 6, 2>(a);
+        if (err == cudaSuccess || err == cudaErrorInvalidValue) return err;
+        cudaGetLastError();  // no room for a pair of CTAs: single SMs
+    }
+    return launch_wgrad<false, F32, 4, 2>(a);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_wgrad(const LinearBwdArgs& a) {
+    return a.dw_dt == MOE_F32 ? launch_typed<true>(a) : launch_typed<false>(a);
+}
+
+}  // namespace moe

@@ -33,9 +33,9 @@ bool optional_ok(const void* p) { return aligned16(p); }  // null is aligned
 
 // Workspace regions (1 KiB aligned): status word, counters.
 struct LinearWs {
-    size_t status, counters, partials, dz, total;
+    size_t status, counters, partials, dz, dz_tail, x_tail, db_part, total;
 };
-LinearWs linear_ws(int rows, int N, moe_dtype dt, bool backward) {
+LinearWs linear_ws(int rows, int K, int N, int E, moe_dtype dt, bool backward) {
     LinearWs L{};
     size_t o = 0;
     auto take = [&](size_t bytes) {
@@ -46,7 +46,11 @@ LinearWs linear_ws(int rows, int N, moe_dtype dt, bool backward) {
     L.status = take(256);
     L.counters = take(kLinearCounters * 4);
     L.partials = take(dt == MOE_BF16 ? linear_partial_floats(rows) * 4 : 0);
-    L.dz = take(backward ? static_cast<size_t>(rows) * N * 2 : 0);
+    const size_t b = backward ? 1 : 0, tail = b * E * kTailRows;
+    L.dz = take(b * rows * N * 2);
+    L.dz_tail = take(tail * N * 2);
+    L.x_tail = take(tail * K * 2);
+    L.db_part = take(b * linear_chunks(rows, E) * N * 4);
     L.total = o;
     return L;
 }
@@ -88,7 +92,7 @@ moe_status linear_impl(const char* name, bool train, const void* x, const int32_
         !optional_ok(offsets) || (offsets == nullptr && E != 1))
         return MOE_ERR_INVALID_ARG;
     if (train && !ptrs_ok({codes, scales})) return MOE_ERR_INVALID_ARG;
-    const LinearWs L = linear_ws(rows, N, dt, false);
+    const LinearWs L = linear_ws(rows, K, N, E, dt, false);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
     Range range(name);
     LinearArgs a{};
@@ -123,7 +127,7 @@ extern "C" {
 
 size_t moe_grouped_linear_workspace_bytes(int rows, int K, int N, int E, moe_dtype dt) {
     if (check_linear(rows, K, N, E, dt) != MOE_OK) return 0;
-    return linear_ws(rows, N, dt, false).total;
+    return linear_ws(rows, K, N, E, dt, false).total;
 }
 
 moe_status moe_grouped_linear(const void* x, const int32_t* offsets, const void* W,
@@ -167,7 +171,7 @@ moe_status moe_checkpoint_restore(const int8_t* codes, const float* scales, int 
 
 size_t moe_grouped_linear_backward_workspace_bytes(int rows, int K, int N, int E, moe_dtype dt) {
     if (check_linear(rows, K, N, E, dt) != MOE_OK || dt != MOE_BF16) return 0;
-    return linear_ws(rows, N, dt, true).total;
+    return linear_ws(rows, K, N, E, dt, true).total;
 }
 
 moe_status moe_grouped_linear_backward(const void* dy, const void* x, const int32_t* offsets,
@@ -192,7 +196,7 @@ moe_status moe_grouped_linear_backward(const void* dy, const void* x, const int3
     }
     if (!ptrs_ok({dy, x, W, ws})) return MOE_ERR_INVALID_ARG;
     if (act != MOE_ACT_NONE && !ptrs_ok({codes, scales})) return MOE_ERR_INVALID_ARG;
-    const LinearWs L = linear_ws(rows, N, dt, true);
+    const LinearWs L = linear_ws(rows, K, N, E, dt, true);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
     Range range("moe_grouped_linear_backward");
     LinearBwdArgs a{};
@@ -212,6 +216,9 @@ moe_status moe_grouped_linear_backward(const void* dy, const void* x, const int3
     a.dW = dW;
     a.db = db;
     a.dz = at<void>(ws, L.dz);
+    a.dz_tail = at<void>(ws, L.dz_tail);
+    a.x_tail = at<void>(ws, L.x_tail);
+    a.db_part = at<float>(ws, L.db_part);
     a.status = at<uint32_t>(ws, L.status);
     a.counters = at<uint32_t>(ws, L.counters);
     a.partials = at<float>(ws, L.partials);

@@ -1,0 +1,161 @@
+// linear_rows.cu -- the element-wise part of the grouped linear backward:
+//   dz = dy act'(z)   with z the value of its 8-bit code; bf16, one rounding
+//   db_e = sum of dz over the group's rows, from the unrounded fp32 values
+// and, for the weight gradient's reduction over rows in blocks of 64, each group's last
+// partial block of dz and of x copied to a buffer where zero rows follow up to the next
+// multiple of 16.  The rows behind a group belong to the next one, or to nobody and may
+// hold anything; this way they are never read as part of a sum.
+//
+// Bound by bytes: dy 2, code 1.125, dz 2 per value.  A thread owns eight columns and
+// walks a chunk of up to 64 rows of one group, four rows' loads in flight, with the
+// column sums in registers; chunk sums are joined by a second launch in chunk order.
+// Without an activation dz is dy itself: only the tails and db are made.
+#include <cuda_bf16.h>
+
+#include "act_checkpoint.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kCols = kThreads * 8;  // columns per block
+
+struct DzArgs {
+    const __nv_bfloat16* dy;
+    const __nv_bfloat16* x;
+    const int32_t* offsets;
+    const int8_t* codes;   // nullptr: dz = dy
+    const float* scales;
+    int rows, K, N, E, act;
+    __nv_bfloat16* dz;
+    __nv_bfloat16* dz_tail;  // nullptr: no tails wanted
+    __nv_bfloat16* x_tail;
+    float* sums;           // db itself or the chunk sums; nullptr: not wanted
+    bool by_group;         // every group has at most one chunk: chunk e is group e
+    int strips;            // column strips of a chunk: the first n_strips of dz, then of x
+    int n_strips;
+};
+
+__global__ void __launch_bounds__(kThreads) linear_dz_kernel(const DzArgs a) {
+    __shared__ int off[kMaxExperts + 1];
+    if (threadIdx.x == 0) load_group_bounds(a.offsets, a.E, a.rows, off);
+    __syncthreads();
+    const int chunk = blockIdx.x / a.strips, strip = blockIdx.x - chunk * a.strips;
+    int e = 0, i = chunk;  // chunk i of group e
+    for (; e < a.E; ++e) {
+        const int chunks = a.by_group ? 1 : (off[e + 1] - off[e] + kTailRows - 1) / kTailRows;
+        if (i < chunks) break;
+        i -= chunks;
+    }
+    if (e == a.E) return;
+    const int row0 = off[e] + i * kTailRows;
+    const int n = min(off[e + 1] - row0, kTailRows);
+    const bool tail = n > 0 && n < kTailRows && a.dz_tail != nullptr;
+    const int n16 = (n + 15) & ~15;
+    const size_t trow = static_cast<size_t>(e) * kTailRows;
+    const float zero[8] = {};
+
+    if (strip >= a.n_strips) {  // x's tail
+        const int c = (strip - a.n_strips) * kCols + threadIdx.x * 8;
+        if (!tail || c >= a.K) return;
+        for (int r = 0; r < n; ++r)
+            *reinterpret_cast<uint4*>(a.x_tail + (trow + r) * a.K + c) =
+                *reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(row0 + r) * a.K + c);
+        for (int r = n; r < n16; ++r) store8(a.x_tail + (trow + r) * a.K + c, zero);
+        return;
+    }
+    const int c = strip * kCols + threadIdx.x * 8;
+    if (c >= a.N) return;
+    const int nb = ckpt_blocks(a.N);
+    float sum[8] = {};
+#pragma unroll 4
+    for (int r = 0; r < n; ++r) {
+        const size_t row = static_cast<size_t>(row0 + r), at = row * a.N + c;
+        float g[8];
+        load8(a.dy + at, g);
+        if (a.codes) {
+            float z[8];
+            ckpt_unpack8(*reinterpret_cast<const uint2*>(a.codes + at),
+                         a.scales[row * nb + c / kCkptBlock], z);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) g[k] *= act_slope(a.act, z[k]);
+            store8(a.dz + at, g);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[k] += g[k];
+        if (tail) store8(a.dz_tail + (trow + r) * a.N + c, g);
+    }
+    if (tail)
+        for (int r = n; r < n16; ++r) store8(a.dz_tail + (trow + r) * a.N + c, zero);
+    if (a.sums)
+        store8(a.sums + static_cast<size_t>(chunk) * a.N + c, sum);
+}
+
+// db[e] = the chunk sums of group e in chunk order: slice s of 8 adds chunks s, s + 8, ..,
+// then the slices are added in order.
+constexpr int kSlices = 8;
+
+__global__ void __launch_bounds__(32 * kSlices)
+    linear_db_kernel(const int32_t* __restrict__ offsets, int rows, int E, int N,
+                     const float* __restrict__ part, float* __restrict__ db) {
+    __shared__ float4 s_sum[kSlices][32];
+    __shared__ int off[kMaxExperts + 1];
+    if (threadIdx.x == 0) load_group_bounds(offsets, E, rows, off);
+    __syncthreads();
+    const int e = blockIdx.y, lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const int c = (blockIdx.x * 32 + lane) * 4;
+    int first = 0;
+    for (int g = 0; g < e; ++g) first += (off[g + 1] - off[g] + kTailRows - 1) / kTailRows;
+    const int chunks = (off[e + 1] - off[e] + kTailRows - 1) / kTailRows;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < N) {
+#pragma unroll 4
+        for (int k = slice; k < chunks; k += kSlices) {
+            const float4 p =
+                *reinterpret_cast<const float4*>(part + static_cast<size_t>(first + k) * N + c);
+            s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+        }
+    }
+    s_sum[slice][lane] = s;
+    __syncthreads();
+    if (slice != 0 || c >= N) return;
+    for (int k = 1; k < kSlices; ++k) {
+        const float4 p = s_sum[k][lane];
+        s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+    }
+    *reinterpret_cast<float4*>(db + static_cast<size_t>(e) * N + c) = s;
+}
+
+}  // namespace
+
+cudaError_t launch_linear_dz(const LinearBwdArgs& a) {
+    if (a.codes == nullptr && a.dW == nullptr && a.db == nullptr) return cudaSuccess;
+    DzArgs d{};
+    d.dy = static_cast<const __nv_bfloat16*>(a.dy);
+    d.x = static_cast<const __nv_bfloat16*>(a.x);
+    d.offsets = a.offsets;
+    d.codes = a.codes;
+    d.scales = a.scales;
+    d.rows = a.rows;
+    d.K = a.K;
+    d.N = a.N;
+    d.E = a.E;
+    d.act = a.act;
+    d.dz = static_cast<__nv_bfloat16*>(a.dz);
+    d.dz_tail = a.dW ? static_cast<__nv_bfloat16*>(a.dz_tail) : nullptr;
+    d.x_tail = static_cast<__nv_bfloat16*>(a.x_tail);
+    d.by_group = a.rows <= kTailRows;
+    d.sums = a.db == nullptr ? nullptr : (d.by_group ? a.db : a.db_part);
+    d.n_strips = (a.N + kCols - 1) / kCols;
+    d.strips = d.n_strips + (a.dW ? (a.K + kCols - 1) / kCols : 0);
+    const size_t chunks = d.by_group ? static_cast<size_t>(a.E) : linear_chunks(a.rows, a.E);
+    // rows * N and rows * K below 2^40 keep this below 2^31
+    cudaError_t err = launch_k(linear_dz_kernel, static_cast<unsigned>(chunks * d.strips), kThreads,
+                               0, a.stream, d);
+    if (err == cudaSuccess && a.db != nullptr && !d.by_group)
+        err = launch_k(linear_db_kernel, dim3((a.N + 127) / 128, a.E), 32 * kSlices, 0, a.stream,
+                       a.offsets, a.rows, a.E, a.N, static_cast<const float*>(a.db_part), a.db);
+    return err;
+}
+
+}  // namespace moe

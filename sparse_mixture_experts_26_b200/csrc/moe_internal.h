@@ -336,13 +336,23 @@ struct LinearBwdArgs {
     void* dx;                // or nullptr
     void* dW;                // or nullptr
     float* db;               // or nullptr
-    void* dz;                // bf16 [rows, N] scratch
+    // scratch
+    void* dz;                // bf16 [rows, N]
+    void* dz_tail;           // bf16 [E * kTailRows, N]: each group's last, partial block of
+    void* x_tail;            // bf16 [E * kTailRows, K]  rows, followed by zero rows
+    float* db_part;          // [linear_chunks(rows, E), N]
     uint32_t* status;
     uint32_t* counters;
     float* partials;
     cudaStream_t stream;
 };
+constexpr int kTailRows = 64;
+// Blocks of up to kTailRows rows of one group, at most.
+inline size_t linear_chunks(int rows, int E) { return static_cast<size_t>(rows) / kTailRows + E; }
 cudaError_t launch_linear_backward(const LinearBwdArgs& a);
+// dz, the tails and db (linear_rows.cu); dW from them (grouped_linear_wgrad_sm100.cu).
+cudaError_t launch_linear_dz(const LinearBwdArgs& a);
+cudaError_t launch_linear_wgrad(const LinearBwdArgs& a);
 // The bf16 products over the groups' rows on tensor cores: the forward, and with
 // transposed = true out[r, :] = x[r, :] W_e (W [E, K, N]: the backward's dx).
 cudaError_t launch_linear_bf16(const LinearArgs& a, bool transposed);

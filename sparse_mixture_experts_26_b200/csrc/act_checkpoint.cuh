@@ -11,25 +11,47 @@
 
 namespace moe {
 
+__device__ __forceinline__ float rcp_approx(float v) {  // one step of v's reciprocal
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// The normal distribution Phi(z), with e = exp(-z^2 / 2), by Abramowitz and Stegun 7.1.26
+// (erf x = 1 - (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + p x), off by at most 1.5e-7),
+// for x = |z| / sqrt 2.  No branch, so that eight of them overlap: erff's two ranges, taken
+// in turn by a warp, made the epilogue the bound (K = 2048, GELU: 44,000 cycles a tile
+// against 16,400 of tensor core time).
+__device__ __forceinline__ float normal_cdf(float z, float e) {
+    const float t = rcp_approx(fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
+    float p = fmaf(1.061405429f, t, -1.453152027f);
+    p = fmaf(p, t, 1.421413741f);
+    p = fmaf(p, t, -0.284496736f);
+    p = fmaf(p, t, 0.254829592f);
+    const float tail = 0.5f * p * t * e;  // Phi(-|z|)
+    return z < 0.f ? tail : 1.0f - tail;
+}
+
 // act(z).  A NaN stays a NaN in every form.
 __device__ __forceinline__ float act_value(int act, float z) {
     if (act == MOE_ACT_RELU) return z <= 0.f ? 0.f : z;
-    if (act == MOE_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    if (act == MOE_ACT_SILU) return z * __frcp_rn(1.0f + __expf(-z));
+    if (act == MOE_ACT_GELU) return z * normal_cdf(z, __expf(-0.5f * z * z));
+    if (act == MOE_ACT_SILU) return z * rcp_approx(1.0f + __expf(-z));
     return z;
 }
 
 // act'(z); the slope of ReLU at 0 is 0.
-//   GELU: Phi(z) + z phi(z), Phi the normal distribution, phi its density
+//   GELU: Phi(z) + z phi(z), phi the normal density
 //   SiLU: s (1 + z (1 - s)), s = 1 / (1 + e^-z)
 __device__ __forceinline__ float act_slope(int act, float z) {
     if (act == MOE_ACT_RELU) return z <= 0.f ? 0.f : (z > 0.f ? 1.f : z);
-    if (act == MOE_ACT_GELU)
-        return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
-               z * (0.39894228040143268f * __expf(-0.5f * z * z));
+    if (act == MOE_ACT_GELU) {
+        const float e = __expf(-0.5f * z * z);
+        return fmaf(0.39894228f * z, e, normal_cdf(z, e));
+    }
     if (act == MOE_ACT_SILU) {
-        const float s = __frcp_rn(1.0f + __expf(-z));
-        return s * (1.0f + z * (1.0f - s));
+        const float s = rcp_approx(1.0f + __expf(-z));
+        return s * fmaf(z, 1.0f - s, 1.0f);
     }
     return 1.f;
 }

@@ -11,10 +11,10 @@
 // are cut into the fewest tiles of at most 256, all of nearly the same width.
 //
 // Layout: every CTA is persistent; warp 0 feeds a ring of TMA stages (64 of the reduction:
-// 128 features, 16 KiB, over the tile's token rows in boxes of 16 or 32), warp 1 issues
-// tcgen05.mma (fp32 accumulator in TMEM, two of 256 columns), warps 2-5 drain the other
+// 128 features, 16 KiB, over the tile's token rows), warp 1 issues
+// tcgen05.mma (fp32 accumulator in TMEM, two of 256 columns), warps 2-9 drain the other
 // accumulator.  The ring's stage size goes by the widest tile of this call, read from
-// `offsets` on the device: 11 stages for 16 tokens, 6 on a pair for 256.  Forward weights
+// `offsets` on the device: 10 stages for 16 tokens, 6 on a pair for 256.  Forward weights
 // are K-major; the transposed product reads the same weights MN-major (64 x 64 boxes).
 //
 // Epilogue: TMEM lanes are features and columns tokens, so 16 columns at a time go through
@@ -23,11 +23,13 @@
 // 128 features are written together, and a checkpoint block of 32 features is four
 // neighbouring lanes (two shuffles for its largest magnitude).
 //
-// Split reduction: tiles are dealt out round by round.  Where the last round would leave
+// Split reduction (single SMs): tiles are dealt out round by round.  Where the last round would leave
 // SMs idle, its tiles are cut along the reduction instead (equal shares of all remaining
 // 64-steps, at most two tiles each): every share's fp32 tile goes to the workspace, and the
 // CTA that finishes a tile last adds the shares in the order of the reduction, whoever it
-// is, so the result does not depend on the timing; nobody waits for anybody.
+// is, so the result does not depend on the timing; nobody waits for anybody.  Pairs do not
+// share: they run at the power limit, where an idle SM lets the others clock higher (4096 x
+// 14336 x 4096: 1286 TFLOP/s unshared, 1232 shared).
 //
 // Every wait is bounded (sm100_ptx.cuh).
 #include <cuda.h>
@@ -51,18 +53,21 @@ constexpr int kBK = 64;                // reduction per stage
 constexpr int kF = 128;                // features per CTA (TMEM lanes)
 constexpr int kTokens = 256;           // most token columns of a tile
 constexpr int kABytes = kF * kBK * 2;  // 16 KiB
-constexpr int kRingBytes = 204 * 1024;
-constexpr int kMaxStages = 11;
-constexpr int kThreads = 192;
-constexpr int kEpiThreads = 128;
+constexpr int kRingBytes = 192 * 1024;
+constexpr int kMaxStages = 10;
+constexpr int kEpiGroup = 128;         // four warps: the 128 lanes of an accumulator
+constexpr int kEpiGroups = 2;          // they take the 16-column rounds in turn
+constexpr int kEpiThreads = kEpiGroup * kEpiGroups;
+constexpr int kThreads = 64 + kEpiThreads;
 constexpr int kRound = 16;             // token columns per epilogue round
 constexpr int kPitch = kF + 4;         // staged token row, floats (16-byte rows)
-constexpr int kStagingBytes = 2 * kRound * kPitch * 4;
+constexpr int kStagingBytes = kEpiGroups * 2 * kRound * kPitch * 4;
 constexpr int kBookBytes = 1024;
 constexpr int kSmemBytes = kRingBytes + kStagingBytes + kBookBytes + 1024 /*align*/;
 static_assert(kSmemBytes <= 232448, "shared memory");
-constexpr int kStageBarrier = 1;
-constexpr int kVoteBarrier = 2;
+constexpr int kVoteBarrier = 1;
+constexpr int kJoinBarrier = 2;
+constexpr int kStageBarrier = 3;       // one for each epilogue group
 constexpr uint16_t kBothCtas = 0x3;
 // A split is worth it from this many 64-steps saved per CTA (below, writing and joining
 // the shares costs more), and a share has at least kMinShare of them.
@@ -87,6 +92,13 @@ struct Args {
     float* partials;
     int slot_tokens;
     uint32_t* status;
+};
+
+// Token rows in boxes of 16, 32, .. 128, so that a tile's half (pair) or its one or two
+// parts arrive with one TMA load each and nothing more is read.
+constexpr int kBoxes = 8;
+struct TokenMaps {
+    CUtensorMap box[kBoxes];
 };
 
 struct Book {
@@ -141,7 +153,7 @@ __device__ __forceinline__ Tile decode_tile(const Book& bk, const Args& a, int f
 // or a share of the remaining `rem` tiles' reduction.
 struct Plan {
     int G, c, num_kb, rounds, rem, share_ctas;
-    __device__ __forceinline__ Plan(int G_, int c_, int total, int num_kb_)
+    __device__ __forceinline__ Plan(int G_, int c_, int total, int num_kb_, bool may_share)
         : G(G_), c(c_), num_kb(num_kb_) {
         rounds = total / G;
         rem = total - rounds * G;
@@ -151,7 +163,7 @@ struct Plan {
             long long most = units / kMinShare;
             if (most > G) most = G;
             // steps saved on the busiest CTA by sharing the last round
-            if (most > rem && num_kb - (units + most - 1) / most >= kMinSaved)
+            if (may_share && most > rem && num_kb - (units + most - 1) / most >= kMinSaved)
                 share_ctas = static_cast<int>(most);
         }
     }
@@ -196,7 +208,7 @@ struct Plan {
 template <bool PAIR, bool TRANSPOSED>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_sm100_kernel(const __grid_constant__ CUtensorMap tmW,
-                        const __grid_constant__ CUtensorMap tmX, const Args args) {
+                        const __grid_constant__ TokenMaps tmX, const Args args) {
     constexpr int kCtas = PAIR ? 2 : 1;
     constexpr int kStep = PAIR ? 32 : 16;
     constexpr int kTileF = kF * kCtas;
@@ -228,7 +240,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmW);
-        tma_prefetch_desc(&tmX);
     }
     if (warp == 1) {
         if (PAIR)
@@ -252,8 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 most = tt > most ? tt : most;
             }
         }
-        const int boxes = (widest / kCtas + args.box - 1) / args.box;
-        bk.stage_bytes = kABytes + boxes * args.box * kBK * 2;
+        bk.stage_bytes = kABytes + widest / kCtas * kBK * 2;
         const int fit = kRingBytes / bk.stage_bytes;
         bk.stages = fit < kMaxStages ? fit : kMaxStages;
         bk.one_tile_each = most <= 1;
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const uint32_t tmem_base = bk.tmem_base;
     const int stages = bk.stages, stage_bytes = bk.stage_bytes;
-    const Plan plan(gridDim.x / kCtas, blockIdx.x / kCtas, bk.tile_start[args.E], num_kb);
+    const Plan plan(gridDim.x / kCtas, blockIdx.x / kCtas, bk.tile_start[args.E], num_kb, !PAIR);
     int tile, kb0, kb1;
 
     if (warp == 0) {
@@ -280,13 +290,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; ok && plan.get(i, tile, kb0, kb1); ++i) {
                 const Tile t = decode_tile<kStep>(bk, args, ftiles, kTileF, tile);
                 const int half = t.nt / kCtas;
-                const int boxes = (half + args.box - 1) / args.box;
+                const int n0 = half < 128 ? half : 128, n1 = half - n0;
+                const CUtensorMap* map0 = &tmX.box[n0 / 16 - 1];
+                const CUtensorMap* map1 = &tmX.box[n1 > 0 ? n1 / 16 - 1 : 0];
                 const int x_row = t.row0 + static_cast<int>(rank) * half;
                 const int f = t.f0 + static_cast<int>(rank) * kF;
-                const uint32_t bytes =
-                    static_cast<uint32_t>(kABytes + boxes * args.box * kBK * 2);
+                const uint32_t bytes = static_cast<uint32_t>(kABytes + half * kBK * 2);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait_bounded(&bk.empty[stage], phase ^ 1u, abort_flag,
+                    if (!mbar_wait_asleep(&bk.empty[stage], phase ^ 1u, abort_flag,
                                            args.status)) {
                         ok = false;
                         break;
@@ -303,9 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             tma_load_3d_pair(&tmW, bar, w, c, f, t.e);
                         }
-                        for (int b = 0; b < boxes; ++b)
-                            tma_load_2d_pair(&tmX, bar, x + b * args.box * kBK * 2, c,
-                                             x_row + b * args.box);
+                        tma_load_2d_pair(map0, bar, x, c, x_row);
                     } else {
                         uint64_t* bar = &bk.full[stage];
                         mbar_arrive_expect_tx(bar, bytes);
@@ -323,9 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             tma_load_3d(&tmW, bar, w, c, f, t.e);
                         }
-                        for (int b = 0; b < boxes; ++b)
-                            tma_load_2d(&tmX, bar, x + b * args.box * kBK * 2, c,
-                                        x_row + b * args.box);
+                        tma_load_2d(map0, bar, x, c, x_row);
+                        if (n1 > 0) tma_load_2d(map1, bar, x + 128 * kBK * 2, c, x_row + 128);
                     }
                     issued = true;
                     pending |= 1u << stage;
@@ -357,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; ok && plan.get(i, tile, kb0, kb1); ++i) {
                 const Tile t = decode_tile<kStep>(bk, args, ftiles, kTileF, tile);
                 const uint32_t idesc = idesc_bf16_f32_major(kTileF, t.nt, TRANSPOSED, false);
-                if (!mbar_wait_bounded(&bk.tmem_empty[acc], acc_phase ^ 1u, abort_flag,
+                if (!mbar_wait_asleep(&bk.tmem_empty[acc], acc_phase ^ 1u, abort_flag,
                                        args.status)) {
                     ok = false;
                     break;
@@ -365,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kTokens);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait_bounded(&bk.full[stage], phase, abort_flag, args.status)) {
+                    if (!mbar_wait_asleep(&bk.full[stage], phase, abort_flag, args.status)) {
                         ok = false;
                         break;
                     }
@@ -414,7 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;
-        const int et = static_cast<int>(threadIdx.x) - 64;  // 0 .. 127
+        const int group = (warp - 2) >> 2;
+        const int et = static_cast<int>(threadIdx.x) - 64 - group * kEpiGroup;  // 0 .. 127
         const int my_tok = et >> 4;                         // token of a round: my_tok, + 8
         const int j = et & 15;                              // features 8 j .. 8 j + 7
         // Two 16-byte reads of the staged row cover eight features; swapping their order in
@@ -430,15 +439,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             else
                 mbar_arrive(&bk.tmem_empty[acc]);
         };
-        auto sync_epilogue = [&]() {
-            asm volatile("bar.sync %0, %1;" ::"n"(kStageBarrier), "n"(kEpiThreads) : "memory");
+        auto sync_group = [&]() {
+            asm volatile("bar.sync %0, %1;" ::"r"(kStageBarrier + group), "n"(kEpiGroup) : "memory");
         };
+        auto sync_epilogue = [&]() {
+            asm volatile("bar.sync %0, %1;" ::"n"(kJoinBarrier), "n"(kEpiThreads) : "memory");
+        };
+        float* my_staging = staging + group * 2 * kRound * kPitch;
         const size_t slot_floats = static_cast<size_t>(kF) * args.slot_tokens;
         int acc = 0, buf = 0;
         uint32_t acc_phase = 0;
         for (int i = 0; plan.get(i, tile, kb0, kb1); ++i) {
             const Tile t = decode_tile<kStep>(bk, args, ftiles, kTileF, tile);
-            if (!bar_all(mbar_wait_bounded(&bk.tmem_full[acc], acc_phase, abort_flag, args.status),
+            if (!bar_all(mbar_wait_asleep(&bk.tmem_full[acc], acc_phase, abort_flag, args.status),
                          kVoteBarrier, kEpiThreads))
                 break;
             tc_fence_after();
@@ -487,15 +500,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
 
             if (kb1 - kb0 == num_kb) {
-                for (int c0 = 0; c0 < t.nt; c0 += kRound) {
+                if (group * kRound >= t.nt) release(acc);  // no round for this group
+                for (int c0 = group * kRound; c0 < t.nt; c0 += kEpiGroups * kRound) {
                     uint32_t r[kRound];
                     tmem_ld_16cols(tbase + c0, r);
                     tmem_ld_wait();
-                    if (c0 + kRound >= t.nt) release(acc);
-                    float* st = staging + buf * kRound * kPitch;
+                    if (c0 + kEpiGroups * kRound >= t.nt) release(acc);
+                    float* st = my_staging + buf * kRound * kPitch;
 #pragma unroll
                     for (int k = 0; k < kRound; ++k) st[k * kPitch + q * 32 + lane] = bits_f32(r[k]);
-                    sync_epilogue();
+                    sync_group();
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int tok = my_tok + 8 * h;
@@ -514,11 +528,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int rem_tile = tile - plan.rounds * plan.G;
                 float* slot = args.partials +
                               static_cast<size_t>((plan.c * 2 + seg) * kCtas + rank) * slot_floats;
-                for (int c0 = 0; c0 < t.nt; c0 += kRound) {
+                if (group * kRound >= t.nt) release(acc);
+                for (int c0 = group * kRound; c0 < t.nt; c0 += kEpiGroups * kRound) {
                     uint32_t r[kRound];
                     tmem_ld_16cols(tbase + c0, r);
                     tmem_ld_wait();
-                    if (c0 + kRound >= t.nt) release(acc);
+                    if (c0 + kEpiGroups * kRound >= t.nt) release(acc);
 #pragma unroll
                     for (int k = 0; k < kRound; ++k)
                         __stcg(slot + (c0 + k) * kF + q * 32 + lane, bits_f32(r[k]));
@@ -528,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t* counter = args.counters + rem_tile * kCtas + rank;
                 __threadfence();
                 sync_epilogue();
-                if (et == 0) {
+                if (threadIdx.x == 64) {
                     const uint32_t before = atomicAdd(counter, 1u);
                     bk.last = before == static_cast<uint32_t>(last - first);
                     if (bk.last) *counter = 0;  // zero again for the next call
@@ -536,19 +551,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sync_epilogue();
                 if (bk.last) {
                     __threadfence();
-                    for (int tok = my_tok; tok < t.nt; tok += 8) {
-                        float v[8] = {};
+                    // kJoin tokens a thread at a time, so that enough loads are in flight
+                    constexpr int kJoin = 4;
+                    for (int tok0 = group * 8 * kJoin + my_tok; tok0 < t.nt;
+                         tok0 += kEpiGroups * 8 * kJoin) {
+                        float v[kJoin][8] = {};
+#pragma unroll 2
                         for (int s = first; s <= last; ++s) {
                             const int sseg = plan.bound(s) / num_kb == rem_tile ? 0 : 1;
                             const float4* src = reinterpret_cast<const float4*>(
                                 args.partials +
                                 static_cast<size_t>((s * 2 + sseg) * kCtas + rank) * slot_floats +
-                                tok * kF + 8 * j);
-                            const float4 lo = __ldcg(src), hi = __ldcg(src + 1);
-                            v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
-                            v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
+                                tok0 * kF + 8 * j);
+                            float4 lo[kJoin], hi[kJoin];
+#pragma unroll
+                            for (int k = 0; k < kJoin; ++k) {
+                                if (tok0 + 8 * k >= t.nt) continue;
+                                lo[k] = __ldcg(src + k * (8 * kF / 4));
+                                hi[k] = __ldcg(src + k * (8 * kF / 4) + 1);
+                            }
+#pragma unroll
+                            for (int k = 0; k < kJoin; ++k) {
+                                if (tok0 + 8 * k >= t.nt) continue;
+                                v[k][0] += lo[k].x, v[k][1] += lo[k].y;
+                                v[k][2] += lo[k].z, v[k][3] += lo[k].w;
+                                v[k][4] += hi[k].x, v[k][5] += hi[k].y;
+                                v[k][6] += hi[k].z, v[k][7] += hi[k].w;
+                            }
                         }
-                        finish(tok, v);
+                        // unrolled: the sums stay in registers
+#pragma unroll
+                        for (int k = 0; k < kJoin; ++k)
+                            if (tok0 + 8 * k < t.nt) finish(tok0 + 8 * k, v[k]);
                     }
                 }
             }
@@ -581,11 +615,11 @@ cudaError_t launch_engine(const LinearArgs& a, int F, int C) {
     g.rows = a.rows;
     g.F = F;
     g.C = C;
-    g.box = a.rows <= kTokens ? 16 : 32;
-    // token rows of a run: at most about 64 MB, half of L2
-    const long long tile_bytes = static_cast<long long>(kTokens) * C * 2;
-    const long long run = (64LL << 20) / tile_bytes;
-    g.group = static_cast<int>(run < 1 ? 1 : (run > 1024 ? 1024 : run));
+    // Token tiles of a run: 32 MB of rows, eight at least, so that the tiles in flight cover
+    // about as many features as tokens and few of either (8192 x 4096 x 14336, one group,
+    // 32 tiles a run: 1263 TFLOP/s, 16: 1372).
+    const long long run = (32LL << 20) / (static_cast<long long>(kTokens) * C * 2);
+    g.group = static_cast<int>(run < 8 ? 8 : (run > 1024 ? 1024 : run));
     g.act = a.act;
     g.bias = static_cast<const __nv_bfloat16*>(a.bias);
     g.residual = static_cast<const __nv_bfloat16*>(a.residual);
@@ -597,10 +631,12 @@ cudaError_t launch_engine(const LinearArgs& a, int F, int C) {
     g.partials = a.partials;
     g.slot_tokens = linear_slot_tokens(a.rows);
     g.status = a.status;
-    CUtensorMap w, x;
-    if (!(TRANSPOSED ? encode_bf16_3d(&w, a.W, a.E, C, F, 64) : encode_bf16_3d(&w, a.W, a.E, F, C, kF)) ||
-        !encode_bf16_2d(&x, a.x, a.rows, C, g.box))
+    CUtensorMap w;
+    TokenMaps x;
+    if (!(TRANSPOSED ? encode_bf16_3d(&w, a.W, a.E, C, F, 64) : encode_bf16_3d(&w, a.W, a.E, F, C, kF)))
         return cudaErrorInvalidValue;
+    for (int b = 0; b < kBoxes && (b == 0 || 16 * b < a.rows); ++b)  // the sizes tiles can have
+        if (!encode_bf16_2d(&x.box[b], a.x, a.rows, C, 16 * (b + 1))) return cudaErrorInvalidValue;
     int sms = device_sm_count();
     if (sms > kLinearMaxCtas) sms = kLinearMaxCtas;
     // Most tiles there can be: the groups' token tiles, each with its feature tiles.  A

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int mc = m0 + rank * kM;
                 const int nc = n0 + rank * (S::kBBoxes * 64);
                 for (int r = 0; r < n; r += kRows) {
-                    if (!mbar_wait_bounded(&bk.empty[stage], phase ^ 1u, abort_flag,
+                    if (!mbar_wait_asleep(&bk.empty[stage], phase ^ 1u, abort_flag,
                                            args.status)) {
                         ok = false;
                         break;
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int tile = first; ok && tile < total; tile += step) {
                 tile_of(tile, e, m0, n0, row0, n);
                 if (n == 0) continue;  // zeros, written by the epilogue alone
-                if (!mbar_wait_bounded(&bk.tmem_empty[acc], acc_phase ^ 1u, abort_flag,
+                if (!mbar_wait_asleep(&bk.tmem_empty[acc], acc_phase ^ 1u, abort_flag,
                                        args.status)) {
                     ok = false;
                     break;
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kN);
                 for (int r = 0; r < n; r += kRows) {
-                    if (!mbar_wait_bounded(&bk.full[stage], phase, abort_flag, args.status)) {
+                    if (!mbar_wait_asleep(&bk.full[stage], phase, abort_flag, args.status)) {
                         ok = false;
                         break;
                     }
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int tile = first; tile < total; tile += step) {
             tile_of(tile, e, m0, n0, row0, n);
             if (n > 0) {
-                if (!bar_all(mbar_wait_bounded(&bk.tmem_full[acc], acc_phase, abort_flag,
+                if (!bar_all(mbar_wait_asleep(&bk.tmem_full[acc], acc_phase, abort_flag,
                                                args.status),
                              kVoteBarrier, kEpiThreads))
                     break;

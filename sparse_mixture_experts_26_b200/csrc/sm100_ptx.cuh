@@ -80,6 +80,36 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
     }
 }
 
+// The same with a suspend-time hint: the thread sleeps in the barrier until the phase
+// completes or about 1 ms has passed, instead of polling.  Polling warps cost power: under
+// the 1000 W limit a tensor-bound kernel runs 6-9% faster this way (grouped linear, 8192 x
+// 4096 x 14336, one group: 1204 -> 1303 TFLOP/s).
+__device__ __forceinline__ bool mbar_wait_asleep(uint64_t* bar, uint32_t parity,
+                                                 volatile int* abort_flag, uint32_t* status) {
+    auto try_wait = [&]() {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+            : "memory");
+        return done != 0;
+    };
+    if (try_wait()) return true;
+    const unsigned long long t0 = global_timer_ns();
+    while (!try_wait()) {
+        if (*abort_flag) return false;
+        if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+            *abort_flag = 1;
+            if (status) atomicOr(status, 1u);  // MOE_DEV_FLAG_TIMEOUT
+            return false;
+        }
+    }
+    return true;
+}
+
 // Bounded wait used only while tearing down after an abort (no flag, no status).
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
     const unsigned long long t0 = global_timer_ns();

@@ -530,6 +530,20 @@ def _check_checkpoint(codes, scales, rows: int, N: int) -> None:
             torch.float32)
 
 
+def _call(fn: str, tensors, stream, *args) -> None:
+    """Call ``fn(*args, stream)`` under the tensors' device.  Small batches spend their time
+    here, so the device is switched only if another one is current, and the current stream
+    is read as a bare handle."""
+    dev = _dev(*[t for t in tensors if t is not None])
+    if torch.cuda.current_device() == dev.index:
+        handle = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None
+                  else _stream(stream))
+        _check(fn, getattr(_lib, fn)(*args, handle))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, getattr(_lib, fn)(*args, _stream(stream)))
+
+
 def _linear_dims(x, offsets, W, bias):
     if x.dim() != 2 or W.dim() != 3:
         raise ValueError("x must be [rows, K] and W [E, N, K]")
@@ -554,12 +568,10 @@ def _linear(fn, x, offsets, W, y, ws, bias, residual, act, codes, scales, stream
     if residual is not None:
         _expect("residual", residual, (rows, N), x.dtype)
     _ws("ws", ws)
-    tensors = [t for t in (x, offsets, W, y, ws, bias, residual, codes, scales) if t is not None]
     kept = () if codes is None else (_ptr(codes), _ptr(scales))
-    with torch.cuda.device(_dev(*tensors)):
-        _check(fn, getattr(_lib, fn)(_ptr(x), _ptr(offsets), _ptr(W), _ptr(bias), _ptr(residual),
-                                     rows, K, N, E, _act(act), dt, y_dt, _ptr(y), *kept, _ptr(ws),
-                                     ws.numel(), _stream(stream)))
+    _call(fn, (x, offsets, W, y, ws, bias, residual, codes, scales), stream,
+          _ptr(x), _ptr(offsets), _ptr(W), _ptr(bias), _ptr(residual), rows, K, N, E, _act(act),
+          dt, y_dt, _ptr(y), *kept, _ptr(ws), ws.numel())
 
 
 def moe_grouped_linear(x, offsets, W, y, ws, bias=None, residual=None, act: str = "none",
@@ -598,9 +610,8 @@ def moe_checkpoint_save(v, codes, scales, stream=None) -> None:
     rows, N = v.shape
     _check_checkpoint(codes, scales, rows, N)
     dt = _dt(v)
-    with torch.cuda.device(_dev(v, codes, scales)):
-        _check("moe_checkpoint_save", _lib.moe_checkpoint_save(
-            _ptr(v), rows, N, dt, _ptr(codes), _ptr(scales), _stream(stream)))
+    _call("moe_checkpoint_save", (v, codes, scales), stream,
+          _ptr(v), rows, N, dt, _ptr(codes), _ptr(scales))
 
 
 def moe_checkpoint_restore(codes, scales, out, act: str = "none", stream=None) -> None:
@@ -610,9 +621,8 @@ def moe_checkpoint_restore(codes, scales, out, act: str = "none", stream=None) -
     rows, N = out.shape
     _check_checkpoint(codes, scales, rows, N)
     dt = _dt(out)
-    with torch.cuda.device(_dev(codes, scales, out)):
-        _check("moe_checkpoint_restore", _lib.moe_checkpoint_restore(
-            _ptr(codes), _ptr(scales), rows, N, _act(act), dt, _ptr(out), _stream(stream)))
+    _call("moe_checkpoint_restore", (codes, scales, out), stream,
+          _ptr(codes), _ptr(scales), rows, N, _act(act), dt, _ptr(out))
 
 
 def moe_grouped_linear_backward(dy, x, offsets, W, ws, dx=None, dW=None, db=None, codes=None,
@@ -635,9 +645,6 @@ def moe_grouped_linear_backward(dy, x, offsets, W, ws, dx=None, dW=None, db=None
     if codes is not None:
         _check_checkpoint(codes, scales, rows, N)
     _ws("ws", ws)
-    tensors = [t for t in (dy, x, offsets, W, ws, dx, dW, db, codes, scales) if t is not None]
-    with torch.cuda.device(_dev(*tensors)):
-        _check("moe_grouped_linear_backward", _lib.moe_grouped_linear_backward(
-            _ptr(dy), _ptr(x), _ptr(offsets), _ptr(W), _ptr(codes), _ptr(scales), rows, K, N, E,
-            _act(act), dt, dw_dt, _ptr(dx), _ptr(dW), _ptr(db), _ptr(ws), ws.numel(),
-            _stream(stream)))
+    _call("moe_grouped_linear_backward", (dy, x, offsets, W, ws, dx, dW, db, codes, scales),
+          stream, _ptr(dy), _ptr(x), _ptr(offsets), _ptr(W), _ptr(codes), _ptr(scales), rows, K,
+          N, E, _act(act), dt, dw_dt, _ptr(dx), _ptr(dW), _ptr(db), _ptr(ws), ws.numel())

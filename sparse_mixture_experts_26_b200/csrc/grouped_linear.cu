@@ -68,7 +68,9 @@ template <typename T, typename TY>
 __global__ void __launch_bounds__(kThreads) linear_kernel(const LinearArgs a) {
     __shared__ int off[kMaxExperts + 1];
     __shared__ float sz[kT][kT + 1];
-    if (threadIdx.x == 0) load_group_bounds(a.offsets, a.E, a.rows, off);
+    pdl_wait();
+    pdl_launch_dependents();
+    if (threadIdx.x < 32) load_group_bounds(a.offsets, a.E, a.rows, off);
     __syncthreads();
     int e, row0, row_end;
     if (!row_tile(off, a.E, blockIdx.y, e, row0, row_end)) return;
@@ -120,8 +122,7 @@ __global__ void __launch_bounds__(kThreads) linear_kernel(const LinearArgs a) {
             }
         }
         if (!valid) continue;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) z[k] = act_value(a.act, z[k]);
+        act_value8(a.act, z);
         if (a.residual) {
             float r[8];
             load8(static_cast<const T*>(a.residual) + static_cast<size_t>(row) * a.N + n, r);

@@ -12,22 +12,23 @@
 //
 // Layout: every CTA is persistent; warp 0 feeds a ring of TMA stages (64 of the reduction:
 // 128 features, 16 KiB, over the tile's token rows), warp 1 issues
-// tcgen05.mma (fp32 accumulator in TMEM, two of 256 columns), warps 2-9 drain the other
-// accumulator.  The ring's stage size goes by the widest tile of this call, read from
+// tcgen05.mma (fp32 accumulator in TMEM, two of 256 columns), warps 2-17 drain the
+// other accumulator.  The ring's stage size goes by the widest tile of this call, read from
 // `offsets` on the device: 10 stages for 16 tokens, 6 on a pair for 256.  Forward weights
 // are K-major; the transposed product reads the same weights MN-major (64 x 64 boxes).
 //
-// Epilogue: TMEM lanes are features and columns tokens, so 16 columns at a time go through
+// Epilogue: TMEM lanes are features and columns tokens, so eight columns at a time go through
 // shared memory (one bank per lane) and come back with eight consecutive features of one
 // token per thread: bias, residual, activation and the output are 16-byte accesses, a row's
 // 128 features are written together, and a checkpoint block of 32 features is four
 // neighbouring lanes (two shuffles for its largest magnitude).
 //
-// Split reduction (single SMs): tiles are dealt out round by round.  Where the last round would leave
-// SMs idle, its tiles are cut along the reduction instead (equal shares of all remaining
-// 64-steps, at most two tiles each): every share's fp32 tile goes to the workspace, and the
-// CTA that finishes a tile last adds the shares in the order of the reduction, whoever it
-// is, so the result does not depend on the timing; nobody waits for anybody.  Pairs do not
+// Split reduction (single SMs): tiles are dealt out round by round.  Where the last round
+// would leave SMs idle, its tiles are cut along the reduction instead (equal shares of all
+// remaining 64-steps, at most two tiles each): every share's fp32 tile goes to the
+// workspace, and the CTA that finishes a tile last adds the shares in the order of the
+// reduction, whoever it is, so the result does not depend on the timing; nobody waits for
+// anybody.  Pairs do not
 // share: they run at the power limit, where an idle SM lets the others clock higher (4096 x
 // 14336 x 4096: 1286 TFLOP/s unshared, 1232 shared).
 //
@@ -56,10 +57,10 @@ constexpr int kABytes = kF * kBK * 2;  // 16 KiB
 constexpr int kRingBytes = 192 * 1024;
 constexpr int kMaxStages = 10;
 constexpr int kEpiGroup = 128;         // four warps: the 128 lanes of an accumulator
-constexpr int kEpiGroups = 2;          // they take the 16-column rounds in turn
+constexpr int kEpiGroups = 4;          // they take the rounds of columns in turn
 constexpr int kEpiThreads = kEpiGroup * kEpiGroups;
 constexpr int kThreads = 64 + kEpiThreads;
-constexpr int kRound = 16;             // token columns per epilogue round
+constexpr int kRound = 8;              // token columns per epilogue round
 constexpr int kPitch = kF + 4;         // staged token row, floats (16-byte rows)
 constexpr int kStagingBytes = kEpiGroups * 2 * kRound * kPitch * 4;
 constexpr int kBookBytes = 1024;
@@ -149,22 +150,33 @@ __device__ __forceinline__ Tile decode_tile(const Book& bk, const Args& a, int f
     return t;
 }
 
-// The work of CTA (or pair) c of G: `rounds` whole tiles, then either one more whole tile
-// or a share of the remaining `rem` tiles' reduction.
+// The work of CTA (or pair) c of G, in pieces: its share of the last `rem` tiles'
+// reduction (up to two tiles; first, so that joining the shares overlaps the rest), then
+// `rounds` whole tiles; or, without shares, rounds whole tiles and maybe one more.
 struct Plan {
     int G, c, num_kb, rounds, rem, share_ctas;
+    int pieces;             // of this CTA's share: 0, 1 or 2
+    int first, from, to;    // the share: 64-steps from .. to, counted from its first tile
     __device__ __forceinline__ Plan(int G_, int c_, int total, int num_kb_, bool may_share)
         : G(G_), c(c_), num_kb(num_kb_) {
         rounds = total / G;
         rem = total - rounds * G;
-        share_ctas = 0;
-        if (rem > 0) {
+        share_ctas = pieces = first = from = to = 0;
+        if (rem > 0 && may_share) {
             const long long units = static_cast<long long>(rem) * num_kb;
             long long most = units / kMinShare;
             if (most > G) most = G;
             // steps saved on the busiest CTA by sharing the last round
-            if (may_share && most > rem && num_kb - (units + most - 1) / most >= kMinSaved)
+            if (most > rem && num_kb - (units + most - 1) / most >= kMinSaved) {
                 share_ctas = static_cast<int>(most);
+                if (c < share_ctas) {
+                    const long long u0 = bound(c), u1 = bound(c + 1);
+                    first = static_cast<int>(u0 / num_kb);
+                    from = static_cast<int>(u0 - static_cast<long long>(first) * num_kb);
+                    to = from + static_cast<int>(u1 - u0);
+                    pieces = to > num_kb ? 2 : 1;
+                }
+            }
         }
     }
     __device__ __forceinline__ long long bound(int i) const {  // first 64-step of share i
@@ -172,31 +184,19 @@ struct Plan {
     }
     // Piece i of this CTA's work; false when there is none.
     __device__ __forceinline__ bool get(int i, int& tile, int& kb0, int& kb1) const {
+        if (i < pieces) {
+            tile = rounds * G + first + i;
+            kb0 = i == 0 ? from : 0;
+            kb1 = i == 0 ? (to < num_kb ? to : num_kb) : to - num_kb;
+            return true;
+        }
+        i -= pieces;
         kb0 = 0;
         kb1 = num_kb;
-        if (i < rounds) {
-            tile = i * G + c;
-            return true;
-        }
-        i -= rounds;
-        if (share_ctas == 0) {
-            tile = rounds * G + c;
-            return i == 0 && c < rem;
-        }
-        if (c >= share_ctas || i > 1) return false;
-        const long long u0 = bound(c), u1 = bound(c + 1);
-        const long long first = u0 / num_kb;
-        tile = rounds * G + static_cast<int>(first) + i;
-        const long long end = u1 - first * num_kb;  // relative to the first tile's start
-        if (i == 0) {
-            kb0 = static_cast<int>(u0 - first * num_kb);
-            kb1 = end < num_kb ? static_cast<int>(end) : num_kb;
-            return true;
-        }
-        kb1 = static_cast<int>(end - num_kb);
-        return kb1 > 0;
+        tile = i * G + c;
+        return i < rounds || (i == rounds && share_ctas == 0 && c < rem);
     }
-    // Shares first .. last hold remaining tile t.
+    // The share that holds the remaining tiles' 64-step u.
     __device__ __forceinline__ int holder(long long u) const {
         int i = static_cast<int>(u * share_ctas / (static_cast<long long>(rem) * num_kb));
         while (i + 1 < share_ctas && bound(i + 1) <= u) ++i;
@@ -248,25 +248,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_alloc(&bk.tmem_base, kTmemCols);
     }
     pdl_wait();
-    if (threadIdx.x == 0) {
+    pdl_launch_dependents();
+    if (warp == 0) {
         load_group_bounds(args.offsets, args.E, args.rows, bk.off);
-        int widest = kStep, most = 0;
-        bk.tile_start[0] = 0;
-        for (int g = 0; g < args.E; ++g) {
-            const int n = bk.off[g + 1] - bk.off[g];
-            const int tt = (n + kTokens - 1) / kTokens;
-            bk.tile_start[g + 1] = bk.tile_start[g] + tt * ftiles;
-            if (tt > 0) {
-                const int units = (n + kStep - 1) / kStep;
-                const int w = (units + tt - 1) / tt * kStep;
-                widest = w > widest ? w : widest;
-                most = tt > most ? tt : most;
-            }
+        // lane g: group g's token tiles; tile_start is their running sum
+        const int n = lane < args.E ? bk.off[lane + 1] - bk.off[lane] : 0;
+        const int tt = (n + kTokens - 1) / kTokens;
+        int sum = tt;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int below = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += below;
         }
-        bk.stage_bytes = kABytes + widest / kCtas * kBK * 2;
-        const int fit = kRingBytes / bk.stage_bytes;
-        bk.stages = fit < kMaxStages ? fit : kMaxStages;
-        bk.one_tile_each = most <= 1;
+        if (lane < args.E) bk.tile_start[lane + 1] = sum * ftiles;
+        const int units = (n + kStep - 1) / kStep;
+        const int width = tt > 0 ? (units + tt - 1) / tt * kStep : kStep;
+        const int widest = __reduce_max_sync(0xffffffffu, width);
+        const int most = __reduce_max_sync(0xffffffffu, tt);
+        if (lane == 0) {
+            bk.tile_start[0] = 0;
+            bk.stage_bytes = kABytes + widest / kCtas * kBK * 2;
+            const int fit = kRingBytes / bk.stage_bytes;
+            bk.stages = fit < kMaxStages ? fit : kMaxStages;
+            bk.one_tile_each = most <= 1;
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -424,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = warp & 3;
         const int group = (warp - 2) >> 2;
         const int et = static_cast<int>(threadIdx.x) - 64 - group * kEpiGroup;  // 0 .. 127
-        const int my_tok = et >> 4;                         // token of a round: my_tok, + 8
+        const int my_tok = et >> 4;                         // token of a round
         const int j = et & 15;                              // features 8 j .. 8 j + 7
         // Two 16-byte reads of the staged row cover eight features; swapping their order in
         // every other group of four lanes keeps eight lanes on distinct banks.
@@ -483,10 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!valid) return;
-                if (args.act != MOE_ACT_NONE) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = act_value(args.act, v[k]);
-                }
+                act_value8(args.act, v);
                 if (args.residual != nullptr) {
                     float r[8];
                     load8(args.residual + row * args.F + f, r);
@@ -503,35 +505,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (group * kRound >= t.nt) release(acc);  // no round for this group
                 for (int c0 = group * kRound; c0 < t.nt; c0 += kEpiGroups * kRound) {
                     uint32_t r[kRound];
-                    tmem_ld_16cols(tbase + c0, r);
+                    tmem_ld_8cols(tbase + c0, r);
                     tmem_ld_wait();
                     if (c0 + kEpiGroups * kRound >= t.nt) release(acc);
                     float* st = my_staging + buf * kRound * kPitch;
 #pragma unroll
                     for (int k = 0; k < kRound; ++k) st[k * kPitch + q * 32 + lane] = bits_f32(r[k]);
                     sync_group();
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int tok = my_tok + 8 * h;
-                        const float4* src =
-                            reinterpret_cast<const float4*>(st + tok * kPitch + 8 * j);
-                        const float4 p = src[swap], s = src[swap ^ 1];
-                        const float4 lo = swap ? s : p, hi = swap ? p : s;
-                        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                        finish(c0 + tok, v);
-                    }
+                    const float4* src =
+                        reinterpret_cast<const float4*>(st + my_tok * kPitch + 8 * j);
+                    const float4 p = src[swap], s = src[swap ^ 1];
+                    const float4 lo = swap ? s : p, hi = swap ? p : s;
+                    float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    finish(c0 + my_tok, v);
                     buf ^= 1;
                 }
             } else {
                 // a share: the fp32 tile to the workspace as [token][feature]
-                const int seg = i - plan.rounds;
                 const int rem_tile = tile - plan.rounds * plan.G;
                 float* slot = args.partials +
-                              static_cast<size_t>((plan.c * 2 + seg) * kCtas + rank) * slot_floats;
+                              static_cast<size_t>((plan.c * 2 + i) * kCtas + rank) * slot_floats;
                 if (group * kRound >= t.nt) release(acc);
                 for (int c0 = group * kRound; c0 < t.nt; c0 += kEpiGroups * kRound) {
                     uint32_t r[kRound];
-                    tmem_ld_16cols(tbase + c0, r);
+                    tmem_ld_8cols(tbase + c0, r);
                     tmem_ld_wait();
                     if (c0 + kEpiGroups * kRound >= t.nt) release(acc);
 #pragma unroll
@@ -552,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (bk.last) {
                     __threadfence();
                     // kJoin tokens a thread at a time, so that enough loads are in flight
-                    constexpr int kJoin = 4;
+                    constexpr int kJoin = 2;
                     for (int tok0 = group * 8 * kJoin + my_tok; tok0 < t.nt;
                          tok0 += kEpiGroups * 8 * kJoin) {
                         float v[kJoin][8] = {};
@@ -647,20 +644,19 @@ cudaError_t launch_engine(const LinearArgs& a, int F, int C) {
     const long long shares = (C + kBK - 1) / kBK / kMinShare;
     const long long want = tiles * (shares < 1 ? 1 : shares);
     const int units = static_cast<int>(want < sms / kCtas ? want : sms / kCtas);
+    if (!PAIR) return launch_k(kern, units, kThreads, kSmemBytes, a.stream, w, x, g);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(units * kCtas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[1];
-    if (PAIR) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, w, x, g);
     return err != cudaSuccess ? err : cudaGetLastError();
 }

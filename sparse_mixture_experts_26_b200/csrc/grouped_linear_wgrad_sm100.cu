@@ -114,7 +114,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bk.drain, 1);
         bk.abort_flag = 0;
         fence_mbar_init();
-        load_group_bounds(args.offsets, args.E, args.rows, bk.off);
     }
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmZ);
@@ -129,6 +128,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
             tmem_alloc(&bk.tmem_base, kTmemCols);
     }
+    pdl_wait();
+    pdl_launch_dependents();
+    if (warp == 0) load_group_bounds(args.offsets, args.E, args.rows, bk.off);
     tc_fence_before();
     __syncthreads();
     if (PAIR) cluster_sync();
@@ -392,20 +394,19 @@ cudaError_t launch_wgrad(const LinearBwdArgs& a) {
     const long long tiles = static_cast<long long>(a.E) * g.m_tiles * g.n_tiles;
     const int most = device_sm_count() / kCtas;
     const int units = static_cast<int>(tiles < most ? tiles : most);
+    if (!PAIR) return launch_k(kern, units, kThreads, kSmem, a.stream, z, x, zt, xt, o, g);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(units * kCtas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[1];
-    if (PAIR) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, z, x, zt, xt, o, g);
     return err != cudaSuccess ? err : cudaGetLastError();
 }

@@ -6,9 +6,10 @@
 // multiple of 16.  The rows behind a group belong to the next one, or to nobody and may
 // hold anything; this way they are never read as part of a sum.
 //
-// Bound by bytes: dy 2, code 1.125, dz 2 per value.  A thread owns eight columns and
-// walks a chunk of up to 64 rows of one group, four rows' loads in flight, with the
-// column sums in registers; chunk sums are joined by a second launch in chunk order.
+// Bound by bytes: dy 2, code 1.125, dz 2 per value.  A block takes 256 columns of a chunk of
+// up to 64 rows of one group: a warp reads 512 bytes of a row, eight columns a lane, and the
+// eight warps take the rows in turn, so a thread has at most eight rows, all in flight.  The
+// warps' column sums are added in order in shared memory, the chunks' by a second launch.
 // Without an activation dz is dy itself: only the tails and db are made.
 #include <cuda_bf16.h>
 
@@ -17,8 +18,9 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kCols = kThreads * 8;  // columns per block
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCols = 256;  // columns per block
 
 struct DzArgs {
     const __nv_bfloat16* dy;
@@ -38,7 +40,11 @@ struct DzArgs {
 
 __global__ void __launch_bounds__(kThreads) linear_dz_kernel(const DzArgs a) {
     __shared__ int off[kMaxExperts + 1];
-    if (threadIdx.x == 0) load_group_bounds(a.offsets, a.E, a.rows, off);
+    __shared__ __align__(16) float s_sum[kWarps][kCols];  // written 16 bytes at a time
+    pdl_wait();
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0) load_group_bounds(a.offsets, a.E, a.rows, off);
     __syncthreads();
     const int chunk = blockIdx.x / a.strips, strip = blockIdx.x - chunk * a.strips;
     int e = 0, i = chunk;  // chunk i of group e
@@ -56,39 +62,69 @@ __global__ void __launch_bounds__(kThreads) linear_dz_kernel(const DzArgs a) {
     const float zero[8] = {};
 
     if (strip >= a.n_strips) {  // x's tail
-        const int c = (strip - a.n_strips) * kCols + threadIdx.x * 8;
+        const int c = (strip - a.n_strips) * kCols + lane * 8;
         if (!tail || c >= a.K) return;
-        for (int r = 0; r < n; ++r)
-            *reinterpret_cast<uint4*>(a.x_tail + (trow + r) * a.K + c) =
-                *reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(row0 + r) * a.K + c);
-        for (int r = n; r < n16; ++r) store8(a.x_tail + (trow + r) * a.K + c, zero);
+#pragma unroll 4
+        for (int r = warp; r < n16; r += kWarps) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (r < n)
+                v = *reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(row0 + r) * a.K + c);
+            *reinterpret_cast<uint4*>(a.x_tail + (trow + r) * a.K + c) = v;
+        }
         return;
     }
-    const int c = strip * kCols + threadIdx.x * 8;
-    if (c >= a.N) return;
+    const int c = strip * kCols + lane * 8;
+    const bool have = c < a.N;
     const int nb = ckpt_blocks(a.N);
     float sum[8] = {};
-#pragma unroll 4
-    for (int r = 0; r < n; ++r) {
-        const size_t row = static_cast<size_t>(row0 + r), at = row * a.N + c;
-        float g[8];
-        load8(a.dy + at, g);
-        if (a.codes) {
-            float z[8];
-            ckpt_unpack8(*reinterpret_cast<const uint2*>(a.codes + at),
-                         a.scales[row * nb + c / kCkptBlock], z);
+    if (have) {
+        constexpr int kFlight = 4;  // rows whose loads are in flight together
+        for (int r0 = warp; r0 < n; r0 += kFlight * kWarps) {
+            uint4 dy[kFlight];
+            uint2 q[kFlight];
+            float s[kFlight];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) g[k] *= act_slope(a.act, z[k]);
-            store8(a.dz + at, g);
+            for (int k = 0; k < kFlight; ++k) {
+                const int r = r0 + k * kWarps;
+                if (r >= n) continue;
+                const size_t row = static_cast<size_t>(row0 + r), at = row * a.N + c;
+                dy[k] = *reinterpret_cast<const uint4*>(a.dy + at);
+                if (a.codes) {
+                    q[k] = *reinterpret_cast<const uint2*>(a.codes + at);
+                    s[k] = a.scales[row * nb + c / kCkptBlock];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) {
+                const int r = r0 + k * kWarps;
+                if (r >= n) continue;
+                float g[8] = {bf16_lo(dy[k].x), bf16_hi(dy[k].x), bf16_lo(dy[k].y),
+                              bf16_hi(dy[k].y), bf16_lo(dy[k].z), bf16_hi(dy[k].z),
+                              bf16_lo(dy[k].w), bf16_hi(dy[k].w)};
+                if (a.codes) {
+                    float z[8];
+                    ckpt_unpack8(q[k], s[k], z);
+                    act_slope8(a.act, z, g);
+                    store8(a.dz + static_cast<size_t>(row0 + r) * a.N + c, g);
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) sum[u] += g[u];
+                if (tail) store8(a.dz_tail + (trow + r) * a.N + c, g);
+            }
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum[k] += g[k];
-        if (tail) store8(a.dz_tail + (trow + r) * a.N + c, g);
+        if (tail)
+            for (int r = n + warp; r < n16; r += kWarps)
+                store8(a.dz_tail + (trow + r) * a.N + c, zero);
     }
-    if (tail)
-        for (int r = n; r < n16; ++r) store8(a.dz_tail + (trow + r) * a.N + c, zero);
-    if (a.sums)
-        store8(a.sums + static_cast<size_t>(chunk) * a.N + c, sum);
+    if (a.sums == nullptr) return;
+    store8(&s_sum[warp][lane * 8], sum);
+    __syncthreads();
+    const int col = strip * kCols + threadIdx.x;
+    if (col >= a.N) return;
+    float total = s_sum[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) total += s_sum[w][threadIdx.x];
+    a.sums[static_cast<size_t>(chunk) * a.N + col] = total;
 }
 
 // db[e] = the chunk sums of group e in chunk order: slice s of 8 adds chunks s, s + 8, ..,
@@ -100,7 +136,9 @@ __global__ void __launch_bounds__(32 * kSlices)
                      const float* __restrict__ part, float* __restrict__ db) {
     __shared__ float4 s_sum[kSlices][32];
     __shared__ int off[kMaxExperts + 1];
-    if (threadIdx.x == 0) load_group_bounds(offsets, E, rows, off);
+    pdl_wait();
+    pdl_launch_dependents();
+    if (threadIdx.x < 32) load_group_bounds(offsets, E, rows, off);
     __syncthreads();
     const int e = blockIdx.y, lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const int c = (blockIdx.x * 32 + lane) * 4;

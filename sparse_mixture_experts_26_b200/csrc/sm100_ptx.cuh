@@ -389,6 +389,15 @@ __device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_8cols(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+}
+
 // Load 16 TMEM lanes x 64 fp32 columns (shape 16x256b, 8 repetitions of 8 columns)
 // starting at `taddr` (whose lane field selects the first of the 16 lanes, inside this
 // warp's 32-lane quarter).  Thread t receives lanes t/4 and t/4 + 8 of the 16, columns

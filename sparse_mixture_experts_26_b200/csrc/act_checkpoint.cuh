@@ -88,13 +88,26 @@ __device__ __forceinline__ void act_slope8(int act, const float (&z)[8], float (
 constexpr int kCkptBlock = MOE_CHECKPOINT_BLOCK;
 inline __host__ __device__ int ckpt_blocks(int n) { return (n + kCkptBlock - 1) / kCkptBlock; }
 
-// Largest magnitude of a block as its bit pattern: magnitudes order like their bits, and
-// an infinity or NaN is the largest of all, so that it survives into the scale.
-__device__ __forceinline__ uint32_t ckpt_mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// Largest magnitude of eight values; a NaN is larger than all, so that it reaches the scale.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float ckpt_amax8(const float (&v)[8]) {
+    float m = fabsf(v[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(v[i]));
+    return m;
+}
+// .. and of the block that four neighbouring lanes hold.  The whole warp calls this.
+__device__ __forceinline__ float ckpt_amax_block(float m) {
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
 
 // s = amax / 128 (exact); 0 below 2^-100, where 1 / s could overflow.
-__device__ __forceinline__ float ckpt_scale(uint32_t mag) {
-    const float amax = __uint_as_float(mag);
+__device__ __forceinline__ float ckpt_scale(float amax) {
     return amax < 0x1p-100f ? 0.f : amax * 0.0078125f;
 }
 
@@ -114,16 +127,31 @@ __device__ __forceinline__ uint32_t ckpt_code(float v, float s, float inv) {
     return s > 0.f ? __float_as_uint(q + kMagic) : 0u;
 }
 
-// Eight codes of consecutive values as two words, and back.
+__device__ __forceinline__ uint2 ckpt_bytes8(const uint32_t (&c)[8]) {
+    auto four = [](uint32_t a, uint32_t b, uint32_t d, uint32_t e) {
+        return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(d, e, 0x0040), 0x5410);
+    };
+    return make_uint2(four(c[0], c[1], c[2], c[3]), four(c[4], c[5], c[6], c[7]));
+}
+// Eight codes of consecutive values as two words.
 __device__ __forceinline__ uint2 ckpt_pack8(const float (&v)[8], float s) {
     const float inv = ckpt_inverse(s);
     uint32_t c[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = ckpt_code(v[i], s, inv);
-    auto four = [](uint32_t a, uint32_t b, uint32_t d, uint32_t e) {
-        return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(d, e, 0x0040), 0x5410);
-    };
-    return make_uint2(four(c[0], c[1], c[2], c[3]), four(c[4], c[5], c[6], c[7]));
+    return ckpt_bytes8(c);
+}
+// The same for fp32 sums, whose last bits are rounding anyway: one multiply-add that rounds
+// down is the floor, and a reciprocal short of 1 / s by about 2^-22 keeps |v / s| below 128
+// without a clamp.  A value within 2^-15 of a step may take the code below it; the sign is
+// kept.  (15 instructions a value the exact way, 2 this way: training's epilogue at K = 2048
+// is bound by them.)
+__device__ __forceinline__ uint2 ckpt_pack8_sums(const float (&v)[8], float s) {
+    const float inv = ckpt_inverse(s) * (1.0f - 0x1p-22f);
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = __float_as_uint(__fmaf_rd(v[i], inv, 12582912.f));
+    return ckpt_bytes8(c);
 }
 // (q + 1/2) s = q s + s/2 in one rounding.  A byte with its sign bit flipped is q + 128;
 // put below the exponent of 2^23 it is the float 2^23 + 128 + q.

@@ -57,12 +57,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
             const int r = w.row + d + k * w.step;
-            uint32_t mag = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) mag = max(mag, ckpt_mag(x[k][i]));
-            mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
-            mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-            const float s = ckpt_scale(mag);
+            const float s = ckpt_scale(ckpt_amax_block(ckpt_amax8(x[k])));
             if (have && r < rows) {
                 *reinterpret_cast<uint2*>(codes + static_cast<size_t>(r) * N + w.c) =
                     ckpt_pack8(x[k], s);

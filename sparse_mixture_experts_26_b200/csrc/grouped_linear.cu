@@ -107,20 +107,6 @@ __global__ void __launch_bounds__(kThreads) linear_kernel(const LinearArgs a) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) z[k] += b[k];
         }
-        if (a.codes) {
-            uint32_t mag = 0;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) mag = max(mag, ckpt_mag(z[k]));
-            mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
-            mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-            const float s = ckpt_scale(mag);
-            if (valid) {
-                *reinterpret_cast<uint2*>(a.codes + static_cast<size_t>(row) * a.N + n) =
-                    ckpt_pack8(z, s);
-                if ((threadIdx.x & 3) == 0)
-                    a.scales[static_cast<size_t>(row) * ckpt_blocks(a.N) + n / kCkptBlock] = s;
-            }
-        }
         if (!valid) continue;
         act_value8(a.act, z);
         if (a.residual) {

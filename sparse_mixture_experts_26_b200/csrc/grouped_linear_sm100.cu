@@ -14,14 +14,15 @@
 // 128 features, 16 KiB, over the tile's token rows), warp 1 issues
 // tcgen05.mma (fp32 accumulator in TMEM, two of 256 columns), warps 2-17 drain the
 // other accumulator.  The ring's stage size goes by the widest tile of this call, read from
-// `offsets` on the device: 10 stages for 16 tokens, 6 on a pair for 256.  Forward weights
+// `offsets` on the device: 11 stages for 16 tokens, 6 on a pair for 256.  Forward weights
 // are K-major; the transposed product reads the same weights MN-major (64 x 64 boxes).
 //
-// Epilogue: TMEM lanes are features and columns tokens, so eight columns at a time go through
-// shared memory (one bank per lane) and come back with eight consecutive features of one
-// token per thread: bias, residual, activation and the output are 16-byte accesses, a row's
-// 128 features are written together, and a checkpoint block of 32 features is four
-// neighbouring lanes (two shuffles for its largest magnitude).
+// Epilogue: TMEM lanes are features and columns tokens, so a warp turns its 32 features x
+// eight tokens at a time in shared memory of its own (rows of 36 floats: neither side meets
+// a bank twice) and comes back with eight consecutive features of one token per thread:
+// bias, residual, activation and the output are 16-byte accesses, 64 bytes of a row
+// together, and a checkpoint block of 32 features is four neighbouring lanes (two shuffles
+// for its largest magnitude).  Sixteen warps, because the rounds are chains of latencies.
 //
 // Split reduction (single SMs): tiles are dealt out round by round.  Where the last round
 // would leave SMs idle, its tiles are cut along the reduction instead (equal shares of all
@@ -54,21 +55,20 @@ constexpr int kBK = 64;                // reduction per stage
 constexpr int kF = 128;                // features per CTA (TMEM lanes)
 constexpr int kTokens = 256;           // most token columns of a tile
 constexpr int kABytes = kF * kBK * 2;  // 16 KiB
-constexpr int kRingBytes = 192 * 1024;
-constexpr int kMaxStages = 10;
-constexpr int kEpiGroup = 128;         // four warps: the 128 lanes of an accumulator
-constexpr int kEpiGroups = 4;          // they take the rounds of columns in turn
-constexpr int kEpiThreads = kEpiGroup * kEpiGroups;
+constexpr int kRingBytes = 204 * 1024;
+constexpr int kMaxStages = 11;
+constexpr int kEpiGroups = 4;          // of four warps, one for each quarter of the lanes;
+constexpr int kEpiWarps = 4 * kEpiGroups;  // they take the rounds of columns in turn
+constexpr int kEpiThreads = 32 * kEpiWarps;
 constexpr int kThreads = 64 + kEpiThreads;
 constexpr int kRound = 8;              // token columns per epilogue round
-constexpr int kPitch = kF + 4;         // staged token row, floats (16-byte rows)
-constexpr int kStagingBytes = kEpiGroups * 2 * kRound * kPitch * 4;
+constexpr int kPitch = 32 + 4;         // staged token row of a warp, floats
+constexpr int kStagingBytes = kEpiWarps * kRound * kPitch * 4;
 constexpr int kBookBytes = 1024;
 constexpr int kSmemBytes = kRingBytes + kStagingBytes + kBookBytes + 1024 /*align*/;
 static_assert(kSmemBytes <= 232448, "shared memory");
 constexpr int kVoteBarrier = 1;
 constexpr int kJoinBarrier = 2;
-constexpr int kStageBarrier = 3;       // one for each epilogue group
 constexpr uint16_t kBothCtas = 0x3;
 // A split is worth it from this many 64-steps saved per CTA (below, writing and joining
 // the shares costs more), and a share has at least kMinShare of them.
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&bk.tmem_full[a], 1);
-            mbar_init(&bk.tmem_empty[a], kCtas * kEpiThreads);
+            mbar_init(&bk.tmem_empty[a], kCtas * kEpiWarps);
         }
         mbar_init(&bk.drain, 1);
         bk.abort_flag = 0;
@@ -428,31 +428,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;
         const int group = (warp - 2) >> 2;
-        const int et = static_cast<int>(threadIdx.x) - 64 - group * kEpiGroup;  // 0 .. 127
-        const int my_tok = et >> 4;                         // token of a round
-        const int j = et & 15;                              // features 8 j .. 8 j + 7
-        // Two 16-byte reads of the staged row cover eight features; swapping their order in
-        // every other group of four lanes keeps eight lanes on distinct banks.
-        const int swap = (j >> 2) & 1;
+        const int my_tok = lane >> 2;                 // this thread's token of a round
+        const int my_f = q * 32 + (lane & 3) * 8;     // and the first of its eight features
+        float* my_staging = staging + (warp - 2) * kRound * kPitch;
+        const float* get = my_staging + my_tok * kPitch + (lane & 3) * 8;
         const int nb = ckpt_blocks(args.F);
         const uint32_t free0 = PAIR ? map_to_cta(smem_u32(&bk.tmem_empty[0]), 0) : 0u;
         const uint32_t free1 = PAIR ? map_to_cta(smem_u32(&bk.tmem_empty[1]), 0) : 0u;
         auto release = [&](int acc) {
             tc_fence_before();
+            __syncwarp();
+            if (lane != 0) return;
             if (PAIR)
-                mbar_arrive_cluster(acc == 0 ? free0 : free1);
+                mbar_arrive_cluster_light(acc == 0 ? free0 : free1);
             else
                 mbar_arrive(&bk.tmem_empty[acc]);
-        };
-        auto sync_group = [&]() {
-            asm volatile("bar.sync %0, %1;" ::"r"(kStageBarrier + group), "n"(kEpiGroup) : "memory");
         };
         auto sync_epilogue = [&]() {
             asm volatile("bar.sync %0, %1;" ::"n"(kJoinBarrier), "n"(kEpiThreads) : "memory");
         };
-        float* my_staging = staging + group * 2 * kRound * kPitch;
         const size_t slot_floats = static_cast<size_t>(kF) * args.slot_tokens;
-        int acc = 0, buf = 0;
+        int acc = 0;
         uint32_t acc_phase = 0;
         for (int i = 0; plan.get(i, tile, kb0, kb1); ++i) {
             const Tile t = decode_tile<kStep>(bk, args, ftiles, kTileF, tile);
@@ -462,63 +458,65 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * kTokens);
-            const int f = t.f0 + static_cast<int>(rank) * kF + 8 * j;
+            const int f = t.f0 + static_cast<int>(rank) * kF + my_f;
             const bool have_f = f < args.F;  // F is a multiple of 8: all eight or none
             float bias[8] = {};
             if (args.bias != nullptr && have_f)
                 load8(args.bias + static_cast<size_t>(t.e) * args.F + f, bias);
-            // the eight sums of token `tok` -> checkpoint, activation, residual, output
-            auto finish = [&](int tok, float (&v)[8]) {
+            // the eight sums of token `tok` -> checkpoint, activation, residual, output; `at`:
+            // where that token's row has feature f
+            const size_t origin = static_cast<size_t>(t.row0) * args.F + f;
+            auto finish = [&](int tok, size_t at, float (&v)[8]) {
                 const bool valid = have_f && tok < t.n;
-                const size_t row = static_cast<size_t>(t.row0 + tok);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] += bias[k];
                 if (args.codes != nullptr) {
-                    uint32_t mag = 0;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) mag = max(mag, ckpt_mag(v[k]));
-                    if (!have_f) mag = 0;
-                    mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
-                    mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-                    const float s = ckpt_scale(mag);
+                    const float s = ckpt_scale(ckpt_amax_block(have_f ? ckpt_amax8(v) : 0.f));
                     if (valid) {
-                        *reinterpret_cast<uint2*>(args.codes + row * args.F + f) =
-                            ckpt_pack8(v, s);
-                        if ((j & 3) == 0) args.scales[row * nb + f / kCkptBlock] = s;
+                        *reinterpret_cast<uint2*>(args.codes + at) = ckpt_pack8_sums(v, s);
+                        if ((lane & 3) == 0)
+                            args.scales[static_cast<size_t>(t.row0 + tok) * nb + f / kCkptBlock] =
+                                s;
                     }
                 }
                 if (!valid) return;
                 act_value8(args.act, v);
                 if (args.residual != nullptr) {
                     float r[8];
-                    load8(args.residual + row * args.F + f, r);
+                    load8(args.residual + at, r);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) v[k] += r[k];
                 }
                 if (args.out_f32)
-                    store8(static_cast<float*>(args.out) + row * args.F + f, v);
+                    store8(static_cast<float*>(args.out) + at, v);
                 else
-                    store8(static_cast<__nv_bfloat16*>(args.out) + row * args.F + f, v);
+                    store8(static_cast<__nv_bfloat16*>(args.out) + at, v);
             };
+            const size_t F = static_cast<size_t>(args.F);
 
             if (kb1 - kb0 == num_kb) {
-                if (group * kRound >= t.nt) release(acc);  // no round for this group
-                for (int c0 = group * kRound; c0 < t.nt; c0 += kEpiGroups * kRound) {
-                    uint32_t r[kRound];
+                // round by round of 8 tokens; the next one's accumulator columns are on their
+                // way while this one is finished
+                size_t at = origin + (group * kRound + my_tok) * F;
+                uint32_t r[kRound];
+                int c0 = group * kRound;
+                if (c0 < t.nt)
                     tmem_ld_8cols(tbase + c0, r);
+                else
+                    release(acc);  // no round for this group
+                for (; c0 < t.nt; c0 += kEpiGroups * kRound) {
                     tmem_ld_wait();
-                    if (c0 + kEpiGroups * kRound >= t.nt) release(acc);
-                    float* st = my_staging + buf * kRound * kPitch;
+                    const int next = c0 + kEpiGroups * kRound;
+                    if (next >= t.nt) release(acc);
+                    __syncwarp();  // the last round's values have been read
 #pragma unroll
-                    for (int k = 0; k < kRound; ++k) st[k * kPitch + q * 32 + lane] = bits_f32(r[k]);
-                    sync_group();
-                    const float4* src =
-                        reinterpret_cast<const float4*>(st + my_tok * kPitch + 8 * j);
-                    const float4 p = src[swap], s = src[swap ^ 1];
-                    const float4 lo = swap ? s : p, hi = swap ? p : s;
-                    float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                    finish(c0 + my_tok, v);
-                    buf ^= 1;
+                    for (int k = 0; k < kRound; ++k) my_staging[k * kPitch + lane] = bits_f32(r[k]);
+                    if (next < t.nt) tmem_ld_8cols(tbase + next, r);
+                    __syncwarp();
+                    float v[8];
+                    load8(get, v);
+                    finish(c0 + my_tok, at, v);
+                    at += kEpiGroups * kRound * F;
                 }
             } else {
                 // a share: the fp32 tile to the workspace as [token][feature]
@@ -550,8 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __threadfence();
                     // kJoin tokens a thread at a time, so that enough loads are in flight
                     constexpr int kJoin = 2;
-                    for (int tok0 = group * 8 * kJoin + my_tok; tok0 < t.nt;
-                         tok0 += kEpiGroups * 8 * kJoin) {
+                    for (int tok0 = group * kRound * kJoin + my_tok; tok0 < t.nt;
+                         tok0 += kEpiGroups * kRound * kJoin) {
                         float v[kJoin][8] = {};
 #pragma unroll 2
                         for (int s = first; s <= last; ++s) {
@@ -559,17 +557,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float4* src = reinterpret_cast<const float4*>(
                                 args.partials +
                                 static_cast<size_t>((s * 2 + sseg) * kCtas + rank) * slot_floats +
-                                tok0 * kF + 8 * j);
+                                tok0 * kF + my_f);
                             float4 lo[kJoin], hi[kJoin];
 #pragma unroll
                             for (int k = 0; k < kJoin; ++k) {
-                                if (tok0 + 8 * k >= t.nt) continue;
-                                lo[k] = __ldcg(src + k * (8 * kF / 4));
-                                hi[k] = __ldcg(src + k * (8 * kF / 4) + 1);
+                                if (tok0 + kRound * k >= t.nt) continue;
+                                lo[k] = __ldcg(src + k * (kRound * kF / 4));
+                                hi[k] = __ldcg(src + k * (kRound * kF / 4) + 1);
                             }
 #pragma unroll
                             for (int k = 0; k < kJoin; ++k) {
-                                if (tok0 + 8 * k >= t.nt) continue;
+                                if (tok0 + kRound * k >= t.nt) continue;
                                 v[k][0] += lo[k].x, v[k][1] += lo[k].y;
                                 v[k][2] += lo[k].z, v[k][3] += lo[k].w;
                                 v[k][4] += hi[k].x, v[k][5] += hi[k].y;
@@ -579,7 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // unrolled: the sums stay in registers
 #pragma unroll
                         for (int k = 0; k < kJoin; ++k)
-                            if (tok0 + 8 * k < t.nt) finish(tok0 + 8 * k, v[k]);
+                            if (tok0 + kRound * k < t.nt)
+                                finish(tok0 + kRound * k, origin + (tok0 + kRound * k) * F, v[k]);
                     }
                 }
             }

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&bk.tmem_full[a], 1);
-            mbar_init(&bk.tmem_empty[a], kCtas * kEpiThreads);
+            mbar_init(&bk.tmem_empty[a], kCtas * 4);
         }
         mbar_init(&bk.drain, 1);
         bk.abort_flag = 0;
@@ -344,10 +344,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (n == 0) continue;
             tc_fence_before();
-            if (PAIR)
-                mbar_arrive_cluster(acc == 0 ? free0 : free1);
-            else
-                mbar_arrive(&bk.tmem_empty[acc]);
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR)
+                    mbar_arrive_cluster_light(acc == 0 ? free0 : free1);
+                else
+                    mbar_arrive(&bk.tmem_empty[acc]);
+            }
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }

@@ -447,6 +447,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                  : "memory");
 }
 
+// The same for a barrier that tells only that this warp has read its tensor memory (after
+// tcgen05.wait::ld and tcgen05.fence::before_thread_sync): with the default scope the arrive
+// does not wait for this thread's global stores, as a release at cluster scope does.
+__device__ __forceinline__ void mbar_arrive_cluster_light(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Pair TMA load: this CTA's tile lands in its own shared memory; the completed bytes
 // are counted on the mbarrier at `bar_cluster_addr` (the leader CTA's barrier).
 __device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_t bar_cluster_addr,

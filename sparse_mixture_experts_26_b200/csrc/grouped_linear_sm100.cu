@@ -18,8 +18,7 @@
 // are K-major; the transposed product reads the same weights MN-major (64 x 64 boxes).
 //
 // Epilogue: TMEM lanes are features and columns tokens, so a warp turns its 32 features x
-// eight tokens at a time in shared memory of its own (rows of 36 floats: neither side meets
-// a bank twice) and comes back with eight consecutive features of one token per thread:
+// eight tokens at a time in shared memory of its own (neither side meets a bank twice) and comes back with eight consecutive features of one token per thread:
 // bias, residual, activation and the output are 16-byte accesses, 64 bytes of a row
 // together, and a checkpoint block of 32 features is four neighbouring lanes (two shuffles
 // for its largest magnitude).  Sixteen warps, because the rounds are chains of latencies.
@@ -122,29 +121,43 @@ struct Tile {
     int e, f0, row0, n, nt;  // n tokens from output row row0 on, nt columns (n rounded up)
 };
 
-// STEP: granularity of a tile's token columns.
+// a / b and the remainder, 0 <= a < 2^31, b > 0: the quotient of the rounded floats is off by
+// a few at most.  (A tile's decode stands between two tiles; integer divisions there cost
+// the tensor cores about 1000 cycles a tile.)
+__device__ __forceinline__ int divide(int a, int b, int& remainder) {
+    int q = __float2int_rd(static_cast<float>(a) * rcp_approx(static_cast<float>(b)));
+    int r = a - q * b;
+    while (r < 0) --q, r += b;
+    while (r >= b) ++q, r -= b;
+    remainder = r;
+    return q;
+}
+
+// `g`: a group at or before the tile's; left at the tile's, since a CTA's tiles come in
+// ascending order.  STEP: granularity of a tile's token columns.
 template <int STEP>
 __device__ __forceinline__ Tile decode_tile(const Book& bk, const Args& a, int ftiles, int fwidth,
-                                            int tile) {
-    int g = 0;
+                                            int tile, int& g) {
     while (g + 1 < a.E && tile >= bk.tile_start[g + 1]) ++g;
     const int local = tile - bk.tile_start[g];
-    const int n = bk.off[g + 1] - bk.off[g];
+    const int row0 = bk.off[g], n = bk.off[g + 1] - row0;
     const int tt = (n + kTokens - 1) / kTokens;
     // token tiles in runs of `group`; inside a run feature tiles are outer and token tiles
     // inner, so that CTAs running together share the weights
-    const int per_full = a.group * ftiles;
-    const int run = local / per_full;
-    const int r = local - run * per_full;
-    const int left = tt - run * a.group;
-    const int width = left < a.group ? left : a.group;
-    const int i = run * a.group + r % width;
-    const int units = (n + STEP - 1) / STEP, base = units / tt, more = units - base * tt;
+    int r = local, first = 0, width = tt;
+    if (tt > a.group) {
+        first = divide(local, a.group * ftiles, r) * a.group;
+        width = tt - first < a.group ? tt - first : a.group;
+    }
+    int i, more;
+    const int ft = divide(r, width, i);
+    i += first;
+    const int base = divide((n + STEP - 1) / STEP, tt, more);
     const int start = (i * base + (i < more ? i : more)) * STEP;
     Tile t;
     t.e = g;
-    t.f0 = (r / width) * fwidth;
-    t.row0 = bk.off[g] + start;
+    t.f0 = ft * fwidth;
+    t.row0 = row0 + start;
     t.nt = (base + (i < more ? 1 : 0)) * STEP;
     t.n = n - start < t.nt ? n - start : t.nt;
     return t;
@@ -202,6 +215,21 @@ struct Plan {
         while (i + 1 < share_ctas && bound(i + 1) <= u) ++i;
         while (i > 0 && bound(i) > u) --i;
         return i;
+    }
+};
+
+// The pieces of a CTA's work one after the other, decoded.
+template <int STEP>
+struct Pieces {
+    int i = -1, g = 0;
+    int tile, kb0, kb1;
+    Tile t;
+    __device__ __forceinline__ bool next(const Plan& plan, const Book& bk, const Args& a,
+                                         int ftiles, int fwidth) {
+        if (++i == plan.pieces) g = 0;  // from the shares back to the first whole tile
+        if (!plan.get(i, tile, kb0, kb1)) return false;
+        t = decode_tile<STEP>(bk, a, ftiles, fwidth, tile, g);
+        return true;
     }
 };
 
@@ -281,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem_base = bk.tmem_base;
     const int stages = bk.stages, stage_bytes = bk.stage_bytes;
     const Plan plan(gridDim.x / kCtas, blockIdx.x / kCtas, bk.tile_start[args.E], num_kb, !PAIR);
-    int tile, kb0, kb1;
+    Pieces<kStep> cur;
+    auto next_piece = [&]() { return cur.next(plan, bk, args, ftiles, kTileF); };
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
@@ -292,8 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // weights that no second token tile reads again leave L2 first
             const bool stream = bk.one_tile_each != 0;
             const uint64_t policy = l2_policy_evict_first();
-            for (int i = 0; ok && plan.get(i, tile, kb0, kb1); ++i) {
-                const Tile t = decode_tile<kStep>(bk, args, ftiles, kTileF, tile);
+            while (ok && next_piece()) {
+                const Tile t = cur.t;
+                const int kb0 = cur.kb0, kb1 = cur.kb1;
                 const int half = t.nt / kCtas;
                 const int n0 = half < 128 ? half : 128, n1 = half - n0;
                 const CUtensorMap* map0 = &tmX.box[n0 / 16 - 1];
@@ -367,9 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true, issued = false;
-            for (int i = 0; ok && plan.get(i, tile, kb0, kb1); ++i) {
-                const Tile t = decode_tile<kStep>(bk, args, ftiles, kTileF, tile);
-                const uint32_t idesc = idesc_bf16_f32_major(kTileF, t.nt, TRANSPOSED, false);
+            while (ok && next_piece()) {
+                const int kb0 = cur.kb0, kb1 = cur.kb1;
+                const uint32_t idesc = idesc_bf16_f32_major(kTileF, cur.t.nt, TRANSPOSED, false);
                 if (!mbar_wait_asleep(&bk.tmem_empty[acc], acc_phase ^ 1u, abort_flag,
                                        args.status)) {
                     ok = false;
@@ -450,19 +480,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const size_t slot_floats = static_cast<size_t>(kF) * args.slot_tokens;
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int i = 0; plan.get(i, tile, kb0, kb1); ++i) {
-            const Tile t = decode_tile<kStep>(bk, args, ftiles, kTileF, tile);
-            if (!bar_all(mbar_wait_asleep(&bk.tmem_full[acc], acc_phase, abort_flag, args.status),
-                         kVoteBarrier, kEpiThreads))
-                break;
-            tc_fence_after();
-            const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                   static_cast<uint32_t>(acc * kTokens);
+        while (next_piece()) {
+            const Tile t = cur.t;
+            const int i = cur.i, tile = cur.tile, kb0 = cur.kb0, kb1 = cur.kb1;
             const int f = t.f0 + static_cast<int>(rank) * kF + my_f;
             const bool have_f = f < args.F;  // F is a multiple of 8: all eight or none
             float bias[8] = {};
             if (args.bias != nullptr && have_f)
                 load8(args.bias + static_cast<size_t>(t.e) * args.F + f, bias);
+            // A warp that gives up leaves alone; only shares, which come before all whole
+            // tiles, have barriers among the warps, and there they leave together.
+            bool ok = __all_sync(0xffffffffu, mbar_wait_asleep(&bk.tmem_full[acc], acc_phase,
+                                                               abort_flag, args.status));
+            const bool whole = kb1 - kb0 == num_kb;
+            if (i < plan.pieces) ok = bar_all(ok, kVoteBarrier, kEpiThreads);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                   static_cast<uint32_t>(acc * kTokens);
             // the eight sums of token `tok` -> checkpoint, activation, residual, output; `at`:
             // where that token's row has feature f
             const size_t origin = static_cast<size_t>(t.row0) * args.F + f;
@@ -494,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             const size_t F = static_cast<size_t>(args.F);
 
-            if (kb1 - kb0 == num_kb) {
+            if (whole) {
                 // round by round of 8 tokens; the next one's accumulator columns are on their
                 // way while this one is finished
                 size_t at = origin + (group * kRound + my_tok) * F;
@@ -506,12 +541,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     release(acc);  // no round for this group
                 for (; c0 < t.nt; c0 += kEpiGroups * kRound) {
                     tmem_ld_wait();
-                    const int next = c0 + kEpiGroups * kRound;
-                    if (next >= t.nt) release(acc);
+                    const int c1 = c0 + kEpiGroups * kRound;
+                    if (c1 >= t.nt) release(acc);
                     __syncwarp();  // the last round's values have been read
 #pragma unroll
                     for (int k = 0; k < kRound; ++k) my_staging[k * kPitch + lane] = bits_f32(r[k]);
-                    if (next < t.nt) tmem_ld_8cols(tbase + next, r);
+                    if (c1 < t.nt) tmem_ld_8cols(tbase + c1, r);
                     __syncwarp();
                     float v[8];
                     load8(get, v);

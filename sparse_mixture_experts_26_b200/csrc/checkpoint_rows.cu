@@ -12,7 +12,7 @@
 // in flight.  A block of threads is 2^lg column groups wide, to fit narrow rows too.
 #include <cuda_bf16.h>
 
-#include "act_checkpoint.cuh"
+#include "linear_device.cuh"
 
 namespace moe {
 namespace {
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads)
             const float s = ckpt_scale(ckpt_amax_block(ckpt_amax8(x[k])));
             if (have && r < rows) {
                 *reinterpret_cast<uint2*>(codes + static_cast<size_t>(r) * N + w.c) =
-                    ckpt_pack8(x[k], s);
+                    sizeof(T) == 2 ? ckpt_pack8_bf16(x[k], s) : ckpt_pack8(x[k], s);
                 if ((w.c & (kCkptBlock - 1)) == 0)
                     scales[static_cast<size_t>(r) * nb + w.c / kCkptBlock] = s;
             }

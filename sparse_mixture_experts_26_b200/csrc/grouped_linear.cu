@@ -5,7 +5,7 @@
 // values each, over steps of 16 of the reduction staged in shared memory as fp32.
 #include <cuda_bf16.h>
 
-#include "act_checkpoint.cuh"
+#include "linear_device.cuh"
 
 namespace moe {
 namespace {

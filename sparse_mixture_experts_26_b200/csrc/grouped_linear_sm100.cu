@@ -36,7 +36,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
-#include "act_checkpoint.cuh"
+#include "linear_device.cuh"
 #include "moe_internal.h"
 #include "sm100_ptx.cuh"
 
@@ -120,18 +120,6 @@ static_assert(sizeof(Book) <= kBookBytes, "bookkeeping reserve");
 struct Tile {
     int e, f0, row0, n, nt;  // n tokens from output row row0 on, nt columns (n rounded up)
 };
-
-// a / b and the remainder, 0 <= a < 2^31, b > 0: the quotient of the rounded floats is off by
-// a few at most.  (A tile's decode stands between two tiles; integer divisions there cost
-// the tensor cores about 1000 cycles a tile.)
-__device__ __forceinline__ int divide(int a, int b, int& remainder) {
-    int q = __float2int_rd(static_cast<float>(a) * rcp_approx(static_cast<float>(b)));
-    int r = a - q * b;
-    while (r < 0) --q, r += b;
-    while (r >= b) ++q, r -= b;
-    remainder = r;
-    return q;
-}
 
 // `g`: a group at or before the tile's; left at the tile's, since a CTA's tiles come in
 // ascending order.  STEP: granularity of a tile's token columns.

@@ -12,17 +12,15 @@
 // load a quarter of a stage.
 //
 // Bound: many rows, the tensor cores (pairs of SMs halve the bytes staged per product);
-// few rows, the gradient's own bytes (E N K elements written once).  The epilogue stages 32
-// rows x 128 bytes per warp and stores them by TMA (rows and columns past the matrix are
-// outside the tensor), with an L2 evict-first hint, since nobody reads them here again.  For
-// few rows the shared memory goes to staging buffers (2 stages, 8 buffers a warp) instead of
-// input stages (4 and 2; pairs 6 and 2).
+// few rows, the gradient's own bytes (E N K elements written once).  The epilogue's warps
+// turn 32 rows x 128 bytes at a time in shared memory and store whole 128-byte lines with
+// the evict-first policy (nobody reads them here again).
 //
 // Roles, accumulators and bounded waits as in grouped_linear_sm100.cu.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
-#include "act_checkpoint.cuh"
+#include "linear_device.cuh"
 #include "moe_internal.h"
 #include "sm100_ptx.cuh"
 
@@ -43,10 +41,7 @@ constexpr int kN = 256;              // inputs per tile
 constexpr int kRows = kTailRows;     // reduction per stage
 constexpr int kBox = kMnBoxBytes;    // 64 columns x 64 rows
 constexpr int kSlab = 16 * 128;      // 64 columns x 16 rows
-constexpr int kThreads = 192;
-constexpr int kEpiThreads = 128;
 constexpr int kChunk = 32 * 128;     // staged output: 32 rows x 128 bytes
-constexpr int kVoteBarrier = 2;
 constexpr uint16_t kBothCtas = 0x3;
 
 struct Args {
@@ -55,6 +50,7 @@ struct Args {
     int M;         // features (dz columns)
     int N;         // inputs (x columns)
     int m_tiles, n_tiles;
+    void* out;     // [E, M, N]
     uint32_t* status;
 };
 
@@ -70,25 +66,28 @@ struct Book {
     int off[kMaxExperts + 1];
 };
 
-template <bool PAIR, int STAGES, int BUFS>
+// GROUPS: epilogue groups of four warps, one for each quarter of the lanes; the groups take
+// the output's 128-byte columns in turn.
+template <bool PAIR, int STAGES, int GROUPS>
 struct Shape {
+    static constexpr int kEpiWarps = 4 * GROUPS;
+    static constexpr int kThreads = 64 + 32 * kEpiWarps;
     static constexpr int kABytes = 2 * kBox;
     static constexpr int kBBoxes = PAIR ? 2 : 4;  // a pair's CTAs hold half of x's columns
     static constexpr int kStageBytes = kABytes + kBBoxes * kBox;
-    static constexpr int kStaging = 4 * BUFS * kChunk;
+    static constexpr int kStaging = kEpiWarps * kChunk;
     static constexpr int kSmem = STAGES * kStageBytes + kStaging + 1024 /*book*/ + 1024 /*align*/;
     static_assert(kSmem <= 232448, "shared memory");
     static_assert(sizeof(Book<STAGES>) <= 1024, "bookkeeping reserve");
 };
 
-template <bool PAIR, bool F32, int STAGES, int BUFS>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool PAIR, bool F32, int STAGES, int GROUPS>
+__global__ void __launch_bounds__(Shape<PAIR, STAGES, GROUPS>::kThreads, 1)
     linear_wgrad_kernel(const __grid_constant__ CUtensorMap tmZ,
                         const __grid_constant__ CUtensorMap tmX,
                         const __grid_constant__ CUtensorMap tmZt,
-                        const __grid_constant__ CUtensorMap tmXt,
-                        const __grid_constant__ CUtensorMap tmO, const Args args) {
-    using S = Shape<PAIR, STAGES, BUFS>;
+                        const __grid_constant__ CUtensorMap tmXt, const Args args) {
+    using S = Shape<PAIR, STAGES, GROUPS>;
     constexpr int kCtas = PAIR ? 2 : 1;
     constexpr uint32_t kIdesc = idesc_bf16_f32_major(kM * kCtas, kN, true, true);
     constexpr uint32_t kTmemCols = 2 * kN;
@@ -109,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&bk.tmem_full[a], 1);
-            mbar_init(&bk.tmem_empty[a], kCtas * 4);
+            mbar_init(&bk.tmem_empty[a], kCtas * S::kEpiWarps);
         }
         mbar_init(&bk.drain, 1);
         bk.abort_flag = 0;
@@ -120,7 +119,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmX);
         tma_prefetch_desc(&tmZt);
         tma_prefetch_desc(&tmXt);
-        tma_prefetch_desc(&tmO);
     }
     if (warp == 1) {
         if (PAIR)
@@ -142,10 +140,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // column tiles innermost: CTAs running together write neighbouring parts of the same
     // gradient rows
     auto tile_of = [&](int tile, int& e, int& m0, int& n0, int& row0, int& n) {
-        e = tile / per_e;
-        const int local = tile - e * per_e;
-        m0 = local / args.n_tiles * (kM * kCtas);
-        n0 = local % args.n_tiles * kN;
+        int local, nt;
+        e = divide(tile, per_e, local);
+        m0 = divide(local, args.n_tiles, nt) * (kM * kCtas);
+        n0 = nt * kN;
         row0 = bk.off[e];
         n = bk.off[e + 1] - row0;
     };
@@ -277,28 +275,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        const int q = warp & 3;
-        uint8_t* wstage = staging + q * BUFS * kChunk;
-        const uint64_t policy = l2_policy_evict_first();
+        const int q = warp & 3, group = (warp - 2) >> 2;
+        uint8_t* st = staging + (warp - 2) * kChunk;
         const uint32_t free0 = PAIR ? map_to_cta(smem_u32(&bk.tmem_empty[0]), 0) : 0u;
         const uint32_t free1 = PAIR ? map_to_cta(smem_u32(&bk.tmem_empty[1]), 0) : 0u;
-        int acc = 0, buf = 0;
+        int acc = 0;
         uint32_t acc_phase = 0;
         for (int tile = first; tile < total; tile += step) {
             tile_of(tile, e, m0, n0, row0, n);
             if (n > 0) {
-                if (!bar_all(mbar_wait_asleep(&bk.tmem_full[acc], acc_phase, abort_flag,
-                                               args.status),
-                             kVoteBarrier, kEpiThreads))
-                    break;
+                if (!__all_sync(0xffffffffu, mbar_wait_asleep(&bk.tmem_full[acc], acc_phase,
+                                                              abort_flag, args.status)))
+                    break;  // a warp that gives up leaves alone
                 tc_fence_after();
             }
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * kN);
             const int mrow = m0 + rank * kM + q * 32;
-            constexpr int kCols = F32 ? 32 : 64;  // output columns per 128-byte chunk
+            constexpr int kEl = F32 ? 4 : 2;
+            constexpr int kCols = 128 / kEl;  // output columns per chunk
+            const size_t row_bytes = static_cast<size_t>(args.N) * kEl;
 #pragma unroll 1
-            for (int c = 0; c < kN; c += kCols) {
+            for (int c = group * kCols; c < kN; c += GROUPS * kCols) {
                 uint4 out[8];  // this lane's row of the chunk
                 if (n == 0) {
 #pragma unroll
@@ -328,19 +326,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (n0 + c >= args.N || mrow >= args.M) continue;  // uniform in the warp
-                uint8_t* st = wstage + buf * kChunk;
-                if (lane == 0) bulk_wait_group_read<BUFS - 1>();  // this buffer has been read
-                __syncwarp();
+                __syncwarp();  // the last chunk has been read
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     *reinterpret_cast<uint4*>(st + lane * 128 + ((i ^ (lane & 7)) << 4)) = out[i];
-                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    tma_store_3d_hint(&tmO, st, n0 + c, mrow, e, policy);
-                    bulk_commit_group();
+                // eight lanes a row: whole 128-byte lines, four rows at a time
+                const int part = lane & 7;
+                const bool have = n0 + c + part * (16 / kEl) < args.N;
+                uint8_t* to = static_cast<uint8_t*>(args.out) +
+                              static_cast<size_t>(e) * args.M * row_bytes +
+                              static_cast<size_t>(n0 + c) * kEl + part * 16;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = i * 4 + (lane >> 3);
+                    const uint4 v =
+                        *reinterpret_cast<const uint4*>(st + r * 128 + ((part ^ (r & 7)) << 4));
+                    if (have && mrow + r < args.M)
+                        __stcs(reinterpret_cast<uint4*>(
+                                   to + static_cast<size_t>(mrow + r) * row_bytes),
+                               v);
                 }
-                if (++buf == BUFS) buf = 0;
             }
             if (n == 0) continue;
             tc_fence_before();
@@ -354,7 +360,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }
-        if (lane == 0) bulk_wait_group<0>();  // every store complete before the block exits
     }
 
     tc_fence_before();
@@ -369,21 +374,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <bool PAIR, bool F32, int STAGES, int BUFS>
+template <bool PAIR, bool F32, int STAGES, int GROUPS>
 cudaError_t launch_wgrad(const LinearBwdArgs& a) {
     constexpr int kCtas = PAIR ? 2 : 1;
-    constexpr int kSmem = Shape<PAIR, STAGES, BUFS>::kSmem;
-    auto kern = linear_wgrad_kernel<PAIR, F32, STAGES, BUFS>;
+    constexpr int kSmem = Shape<PAIR, STAGES, GROUPS>::kSmem;
+    constexpr int kThreads = Shape<PAIR, STAGES, GROUPS>::kThreads;
+    auto kern = linear_wgrad_kernel<PAIR, F32, STAGES, GROUPS>;
     static PerDeviceOnce once;
     if (const cudaError_t err = opt_in_smem(once, kern, kSmem); err != cudaSuccess) return err;
     const void* dz = a.codes ? a.dz : a.dy;
     const uint64_t tails = static_cast<uint64_t>(a.E) * kTailRows;
-    CUtensorMap z, x, zt, xt, o;
+    CUtensorMap z, x, zt, xt;
     if (!encode_bf16_2d(&z, dz, a.rows, a.N, kRows) || !encode_bf16_2d(&x, a.x, a.rows, a.K, kRows) ||
         !encode_bf16_2d(&zt, a.dz_tail, tails, a.N, 16) ||
-        !encode_bf16_2d(&xt, a.x_tail, tails, a.K, 16) ||
-        !(F32 ? encode_f32_3d(&o, a.dW, a.E, a.N, a.K, 32, 32)
-              : encode_bf16_3d(&o, a.dW, a.E, a.N, a.K, 32)))
+        !encode_bf16_2d(&xt, a.x_tail, tails, a.K, 16))
         return cudaErrorInvalidValue;
     Args g{};
     g.offsets = a.offsets;
@@ -393,11 +397,12 @@ cudaError_t launch_wgrad(const LinearBwdArgs& a) {
     g.N = a.K;
     g.m_tiles = (a.N + kM * kCtas - 1) / (kM * kCtas);
     g.n_tiles = (a.K + kN - 1) / kN;
+    g.out = a.dW;
     g.status = a.status;
     const long long tiles = static_cast<long long>(a.E) * g.m_tiles * g.n_tiles;
     const int most = device_sm_count() / kCtas;
     const int units = static_cast<int>(tiles < most ? tiles : most);
-    if (!PAIR) return launch_k(kern, units, kThreads, kSmem, a.stream, z, x, zt, xt, o, g);
+    if (!PAIR) return launch_k(kern, units, kThreads, kSmem, a.stream, z, x, zt, xt, g);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(units * kCtas);
     cfg.blockDim = dim3(kThreads);
@@ -410,24 +415,30 @@ cudaError_t launch_wgrad(const LinearBwdArgs& a) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, z, x, zt, xt, o, g);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, z, x, zt, xt, g);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-// Average rows per group from which a pair of SMs shares a tile, and up to which the
-// output's bytes are the cost.
-constexpr int kPairRowsPerGroup = 256;
-constexpr int kShortRowsPerGroup = 64;
+// Average rows per group from which a pair of SMs shares a tile, if there is a tile for
+// every pair.  Measured at K = 4096, N = 14336, 8 experts, bf16: 32 rows a group 162 us on
+// single SMs and 182 on pairs, 64 rows 199 and 184, 128 rows 213 and 201, 256 rows 313 and
+// 268; one group of 2000 rows with K = N = 1024 (16 tiles of 256 x 256) 25 and 30.
+constexpr int kPairRowsPerGroup = 64;
 
 template <bool F32>
 cudaError_t launch_typed(const LinearBwdArgs& a) {
-    const int mean = a.rows / a.E;
-    if (mean <= kShortRowsPerGroup) return launch_wgrad<false, F32, 2, 8>(a);
-    if (mean >= kPairRowsPerGroup && pair_gemm_enabled()) {
+    const long long pair_tiles =
+        static_cast<long long>(a.E) * ((a.N + 255) / 256) * ((a.K + kN - 1) / kN);
+    if (a.rows / a.E >= kPairRowsPerGroup && pair_tiles >= device_sm_count() / 2 &&
+        pair_gemm_enabled()) {
         const cudaError_t err = launch_wgrad<true, F32, 6, 2>(a);
         if (err == cudaSuccess || err == cudaErrorInvalidValue) return err;
         cudaGetLastError();  // no room for a pair of CTAs: single SMs
     }
+    // Short reductions in bf16 are bound by the epilogue: sixteen warps of it (32 rows, as
+    // above: 149 us against 169 with eight and four stages).  fp32 has half the values per
+    // byte and twice the bytes, where more writers only scatter them (341 against 316 us).
+    if (!F32 && a.rows / a.E < kPairRowsPerGroup) return launch_wgrad<false, F32, 2, 4>(a);
     return launch_wgrad<false, F32, 4, 2>(a);
 }
 

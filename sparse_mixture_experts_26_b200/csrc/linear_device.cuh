@@ -1,5 +1,5 @@
-// act_checkpoint.cuh -- activations of the grouped linear operators, their slopes, and
-// the 8-bit checkpoint format (include/moe.h, MOE_CHECKPOINT_BLOCK).
+// linear_device.cuh -- device code the grouped linear operators share: activations and their
+// slopes, the 8-bit checkpoint format (include/moe.h, MOE_CHECKPOINT_BLOCK), group bounds.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -22,24 +22,56 @@ __device__ __forceinline__ float ex2_approx(float v) {
     return r;
 }
 
-// Phi(-|z|), Phi the normal distribution, and e = exp(-z^2 / 2), by Abramowitz and Stegun
-// 7.1.26 (erf x = 1 - (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + p x), off by at most
-// 1.5e-7) at x = |z| / sqrt 2, with the exponent taken in base 2 of w = |z| sqrt(log2(e) / 2).
-// No branch, so that eight of them overlap: erff's two ranges, taken in turn by a warp, made
-// the epilogue the bound (K = 2048, GELU: 44,000 cycles a tile against 16,400 of tensor core
-// time).  11 instructions and 2 of the special function unit.
-__device__ __forceinline__ float normal_tail(float z, float& e) {
-    const float w = fabsf(z) * 0.84932180f;       // sqrt(log2(e) / 2)
-    e = ex2_approx(-w * w);
-    const float t = rcp_approx(fmaf(0.27273749f, w, 1.0f));  // 0.3275911 / sqrt(log2(e))
-    float p = fmaf(0.5307027145f, t, -0.726576013f);         // the coefficients, halved
-    p = fmaf(p, t, 0.7107068705f);
-    p = fmaf(p, t, -0.142248368f);
-    p = fmaf(p, t, 0.127414796f);
-    return p * t * e;
+// Two floats in a 64-bit register: one instruction works on both.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
-__device__ __forceinline__ float sigmoid(float z) {
-    return rcp_approx(1.0f + ex2_approx(-1.44269504f * z));
+__device__ __forceinline__ void f2_get(F2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 f2_all(float a) { return f2(a, a); }
+
+// Phi(-x) of two x in [0, 24], Phi the normal distribution, and e = exp(-x^2 / 2), by
+// Abramowitz and Stegun 7.1.26 (erf u = 1 - (a1 t + .. + a5 t^5) exp(-u^2), t = 1 / (1 + p u),
+// off by at most 1.5e-7) at u = x / sqrt 2.  The error shrinks with exp(-u^2): less than a
+// bf16 half step relative to Phi(-x) up to x = 6.  No branch (erff's two ranges, taken in
+// turn by a warp, made a GELU epilogue the bound), and one reciprocal for both values: the
+// special function unit does 16 a clock, an eighth of the others.
+__device__ __forceinline__ F2 normal_tails(float x0, float x1, F2& e) {
+    const F2 x = f2(x0, x1);
+    float m0, m1, d0, d1;
+    f2_get(f2_mul(f2_mul(x, x), f2_all(-0.72134752f)), m0, m1);   // -log2(e) / 2
+    e = f2(ex2_approx(m0), ex2_approx(m1));
+    f2_get(f2_fma(x, f2_all(0.23164189f), f2_all(1.0f)), d0, d1);  // p / sqrt 2
+    const float r = rcp_approx(d0 * d1);
+    const F2 t = f2(r * d1, r * d0);
+    F2 p = f2_fma(f2_all(0.5307027145f), t, f2_all(-0.726576013f));  // a5 .. a1, halved
+    p = f2_fma(p, t, f2_all(0.7107068705f));
+    p = f2_fma(p, t, f2_all(-0.142248368f));
+    p = f2_fma(p, t, f2_all(0.127414796f));
+    return f2_mul(f2_mul(p, t), e);
+}
+// 1 / (1 + e^-z) of two z, with one reciprocal; z counts as -43 below that (2e-19), where
+// the product of the two denominators would leave fp32.
+__device__ __forceinline__ void sigmoids(float z0, float z1, float& s0, float& s1) {
+    const float d0 = 1.0f + ex2_approx(-1.44269504f * fmaxf(z0, -43.f));
+    const float d1 = 1.0f + ex2_approx(-1.44269504f * fmaxf(z1, -43.f));
+    const float r = rcp_approx(d0 * d1);
+    s0 = r * d1;
+    s1 = r * d0;
 }
 
 // v = act(v).  A NaN stays one; an infinity gives an infinity or NaN.
@@ -47,14 +79,21 @@ __device__ __forceinline__ float sigmoid(float z) {
 __device__ __forceinline__ void act_value8(int act, float (&v)[8]) {
     if (act == MOE_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float e;
-            const float tail = normal_tail(v[i], e);
-            v[i] = fmaf(-fabsf(v[i]), tail, fmaxf(v[i], 0.f));
+        for (int i = 0; i < 8; i += 2) {
+            F2 e;
+            float t0, t1;
+            f2_get(normal_tails(fminf(fabsf(v[i]), 24.f), fminf(fabsf(v[i + 1]), 24.f), e), t0, t1);
+            v[i] = fmaf(-fabsf(v[i]), t0, fmaxf(v[i], 0.f));
+            v[i + 1] = fmaf(-fabsf(v[i + 1]), t1, fmaxf(v[i + 1], 0.f));
         }
     } else if (act == MOE_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= sigmoid(v[i]);
+        for (int i = 0; i < 8; i += 2) {
+            float s0, s1;
+            sigmoids(v[i], v[i + 1], s0, s1);
+            v[i] *= s0;
+            v[i + 1] *= s1;
+        }
     } else if (act == MOE_ACT_RELU) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = v[i] <= 0.f ? 0.f : v[i];
@@ -67,22 +106,41 @@ __device__ __forceinline__ void act_value8(int act, float (&v)[8]) {
 __device__ __forceinline__ void act_slope8(int act, const float (&z)[8], float (&g)[8]) {
     if (act == MOE_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float e;
-            const float tail = normal_tail(z[i], e);
-            const float phi = fmaf(0.39894228f * z[i], e, 0.5f);
-            g[i] *= phi + copysignf(0.5f - tail, z[i]);
+        for (int i = 0; i < 8; i += 2) {
+            F2 e2;
+            float t[2], e[2];
+            f2_get(normal_tails(fminf(fabsf(z[i]), 24.f), fminf(fabsf(z[i + 1]), 24.f), e2), t[0],
+                   t[1]);
+            f2_get(e2, e[0], e[1]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                g[i + k] *= fmaf(0.39894228f * z[i + k], e[k], 0.5f) +
+                            copysignf(0.5f - t[k], z[i + k]);
         }
     } else if (act == MOE_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float s = sigmoid(z[i]);
-            g[i] *= s * fmaf(z[i], 1.0f - s, 1.0f);
+        for (int i = 0; i < 8; i += 2) {
+            float s[2];
+            sigmoids(z[i], z[i + 1], s[0], s[1]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) g[i + k] *= s[k] * fmaf(z[i + k], 1.0f - s[k], 1.0f);
         }
     } else if (act == MOE_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] *= z[i] <= 0.f ? 0.f : (z[i] > 0.f ? 1.f : z[i]);
+        for (int i = 0; i < 8; ++i) g[i] = z[i] <= 0.f ? 0.f : g[i];
     }
+}
+
+// a / b and the remainder, 0 <= a < 2^31, b > 0: the quotient of the rounded floats is off by
+// a few at most.  (A tile's decode stands between two tiles; integer divisions there cost
+// the tensor cores about 1000 cycles a tile.)
+__device__ __forceinline__ int divide(int a, int b, int& remainder) {
+    int q = __float2int_rd(static_cast<float>(a) * rcp_approx(static_cast<float>(b)));
+    int r = a - q * b;
+    while (r < 0) --q, r += b;
+    while (r >= b) ++q, r -= b;
+    remainder = r;
+    return q;
 }
 
 constexpr int kCkptBlock = MOE_CHECKPOINT_BLOCK;
@@ -140,6 +198,22 @@ __device__ __forceinline__ uint2 ckpt_pack8(const float (&v)[8], float s) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = ckpt_code(v[i], s, inv);
     return ckpt_bytes8(c);
+}
+// The same for bf16 values, in a third of the instructions.  Quotients of two 8-bit
+// significands are whole or at least 2^-8 away from the next whole number above, except for
+// small negative ones below zero: so 2^-10 on top of the product makes up for its rounding,
+// and the sign is put right by hand (the same minimum holds the largest value at 127).
+__device__ __forceinline__ uint2 ckpt_pack8_bf16(const float (&v)[8], float s) {
+    constexpr float kMagic = 12582912.f;
+    const float inv = ckpt_inverse(s);
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float q = __fadd_rd(fmaf(v[i], inv, 0x1p-10f), kMagic);
+        c[i] = __float_as_uint(fminf(q, v[i] < 0.f ? kMagic - 1.f : kMagic + 127.f));
+    }
+    const uint2 w = ckpt_bytes8(c);
+    return s == 0.f ? make_uint2(0u, 0u) : w;
 }
 // The same for fp32 sums, whose last bits are rounding anyway: one multiply-add that rounds
 // down is the floor, and a reciprocal short of 1 / s by about 2^-22 keeps |v / s| below 128

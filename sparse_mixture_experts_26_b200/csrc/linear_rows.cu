@@ -13,7 +13,7 @@
 // Without an activation dz is dy itself: only the tails and db are made.
 #include <cuda_bf16.h>
 
-#include "act_checkpoint.cuh"
+#include "linear_device.cuh"
 
 namespace moe {
 namespace {
@@ -21,6 +21,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCols = 256;  // columns per block
+constexpr int kBlocksPerSm = 5;
 
 struct DzArgs {
     const __nv_bfloat16* dy;
@@ -34,19 +35,17 @@ struct DzArgs {
     __nv_bfloat16* x_tail;
     float* sums;           // db itself or the chunk sums; nullptr: not wanted
     bool by_group;         // every group has at most one chunk: chunk e is group e
+    int items;             // chunks times strips
     int strips;            // column strips of a chunk: the first n_strips of dz, then of x
     int n_strips;
 };
 
-__global__ void __launch_bounds__(kThreads) linear_dz_kernel(const DzArgs a) {
-    __shared__ int off[kMaxExperts + 1];
-    __shared__ __align__(16) float s_sum[kWarps][kCols];  // written 16 bytes at a time
-    pdl_wait();
-    pdl_launch_dependents();
+// One chunk's strip of columns.  All threads of the block call this together.
+__device__ __forceinline__ void dz_item(const DzArgs& a, const int* off, float (*s_sum)[kCols],
+                                        int item) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp == 0) load_group_bounds(a.offsets, a.E, a.rows, off);
-    __syncthreads();
-    const int chunk = blockIdx.x / a.strips, strip = blockIdx.x - chunk * a.strips;
+    int strip;
+    const int chunk = divide(item, a.strips, strip);
     int e = 0, i = chunk;  // chunk i of group e
     for (; e < a.E; ++e) {
         const int chunks = a.by_group ? 1 : (off[e + 1] - off[e] + kTailRows - 1) / kTailRows;
@@ -74,7 +73,7 @@ __global__ void __launch_bounds__(kThreads) linear_dz_kernel(const DzArgs a) {
         return;
     }
     const int c = strip * kCols + lane * 8;
-    const bool have = c < a.N;
+    const bool have = c < a.N && (a.codes || a.sums || tail);  // else nothing to do here
     const int nb = ckpt_blocks(a.N);
     float sum[8] = {};
     if (have) {
@@ -117,6 +116,7 @@ __global__ void __launch_bounds__(kThreads) linear_dz_kernel(const DzArgs a) {
                 store8(a.dz_tail + (trow + r) * a.N + c, zero);
     }
     if (a.sums == nullptr) return;
+    __syncthreads();  // the last item's sums have been read
     store8(&s_sum[warp][lane * 8], sum);
     __syncthreads();
     const int col = strip * kCols + threadIdx.x;
@@ -125,6 +125,16 @@ __global__ void __launch_bounds__(kThreads) linear_dz_kernel(const DzArgs a) {
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) total += s_sum[w][threadIdx.x];
     a.sums[static_cast<size_t>(chunk) * a.N + col] = total;
+}
+
+__global__ void __launch_bounds__(kThreads) linear_dz_kernel(const DzArgs a) {
+    __shared__ int off[kMaxExperts + 1];
+    __shared__ __align__(16) float s_sum[kWarps][kCols];  // written 16 bytes at a time
+    pdl_wait();
+    pdl_launch_dependents();
+    if (threadIdx.x < 32) load_group_bounds(a.offsets, a.E, a.rows, off);
+    __syncthreads();
+    for (int item = blockIdx.x; item < a.items; item += gridDim.x) dz_item(a, off, s_sum, item);
 }
 
 // db[e] = the chunk sums of group e in chunk order: slice s of 8 adds chunks s, s + 8, ..,
@@ -187,9 +197,11 @@ cudaError_t launch_linear_dz(const LinearBwdArgs& a) {
     d.n_strips = (a.N + kCols - 1) / kCols;
     d.strips = d.n_strips + (a.dW ? (a.K + kCols - 1) / kCols : 0);
     const size_t chunks = d.by_group ? static_cast<size_t>(a.E) : linear_chunks(a.rows, a.E);
-    // rows * N and rows * K below 2^40 keep this below 2^31
-    cudaError_t err = launch_k(linear_dz_kernel, static_cast<unsigned>(chunks * d.strips), kThreads,
-                               0, a.stream, d);
+    d.items = static_cast<int>(chunks * d.strips);  // rows * N, rows * K < 2^40: below 2^31
+    // Blocks stay for several items: reading the group bounds takes a block as long as one.
+    const int most = device_sm_count() * kBlocksPerSm;
+    cudaError_t err = launch_k(linear_dz_kernel, d.items < most ? d.items : most, kThreads, 0,
+                               a.stream, d);
     if (err == cudaSuccess && a.db != nullptr && !d.by_group)
         err = launch_k(linear_db_kernel, dim3((a.N + 127) / 128, a.E), 32 * kSlices, 0, a.stream,
                        a.offsets, a.rows, a.E, a.N, static_cast<const float*>(a.db_part), a.db);

@@ -123,6 +123,25 @@ def test_checkpoint_save_and_restore(rows, N, dtype):
             assert bool(((out.double() - ref).abs() <= tol + 1e-40).all())
 
 
+def test_checkpoint_codes_of_every_bf16_quotient():
+    """Every significand of a block's largest value against every bf16 value down to 2^-20 of
+    it, both signs: the codes are the floor of the exact quotient."""
+    sig = torch.arange(128, 256, device="cuda", dtype=torch.float64)
+    vals = (sig[:, None] * 2.0 ** torch.arange(-20, 1, device="cuda")).flatten()
+    vals = torch.cat([vals, -vals, torch.zeros(2, device="cuda")])
+    for scale in (1.0, 2.0 ** -60, 2.0 ** 90):
+        rows = []
+        for top in sig.tolist():
+            v = vals[vals.abs() <= top]
+            v = torch.nn.functional.pad(v, (0, -len(v) % 31)).view(-1, 31)
+            rows.append(torch.cat([torch.full((len(v), 1), top, device="cuda"), v], 1))
+        v = (torch.cat(rows) * scale).to(bf)
+        codes, scales = moe.alloc_checkpoint(*v.shape)
+        moe.moe_checkpoint_save(v, codes, scales)
+        q, s = R.quantise(v)
+        assert torch.equal(scales.double(), s) and torch.equal(codes, q)
+
+
 def test_checkpoint_blocks_with_infinities_and_nans_come_back_as_such():
     v = torch.ones(4, 96, device="cuda")
     v[0, 5] = float("inf")

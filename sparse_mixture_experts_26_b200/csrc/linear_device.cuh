@@ -42,6 +42,11 @@ __device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ F2 f2_all(float a) { return f2(a, a); }
 
 // Phi(-x) of two x in [0, 24], Phi the normal distribution, and e = exp(-x^2 / 2), by
@@ -230,13 +235,14 @@ __device__ __forceinline__ uint2 ckpt_pack8_sums(const float (&v)[8], float s) {
 // (q + 1/2) s = q s + s/2 in one rounding.  A byte with its sign bit flipped is q + 128;
 // put below the exponent of 2^23 it is the float 2^23 + 128 + q.
 __device__ __forceinline__ void ckpt_unpack8(uint2 c, float s, float (&v)[8]) {
-    const float half = 0.5f * s;
+    const F2 scale = f2_all(s), half = f2_all(0.5f * s);
+    const uint32_t w[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t w = (i < 4 ? c.x : c.y) ^ 0x80808080u;
-        const float q =
-            __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7650 | (i & 3))) - 8388736.f;
-        v[i] = fmaf(q, s, half);
+    for (int i = 0; i < 8; i += 2) {
+        const uint32_t q = w[i >> 2];
+        const F2 u = f2(__uint_as_float(__byte_perm(q, 0x4b000000u, 0x7650 | (i & 3))),
+                        __uint_as_float(__byte_perm(q, 0x4b000000u, 0x7651 + (i & 3))));
+        f2_get(f2_fma(f2_add(u, f2_all(-8388736.f)), scale, half), v[i], v[i + 1]);
     }
 }
 

@@ -8,8 +8,8 @@
 // A group starts and ends anywhere.  Its whole blocks come straight from dz and x; the rest
 // comes from the tail buffers (linear_rows.cu), where the group's last rows are followed
 // by zeros up to a multiple of 16, and only that many 16-row steps are issued.  So no row
-// outside the group is ever multiplied, not even by zero, and small groups (decode batches)
-// load a quarter of a stage.
+// outside the group is ever multiplied, not even by zero, and groups of up to 16 rows (decode
+// batches) load a quarter of a stage.
 //
 // Bound: many rows, the tensor cores (pairs of SMs halve the bytes staged per product);
 // few rows, the gradient's own bytes (E N K elements written once).  The epilogue's warps
@@ -38,9 +38,7 @@ namespace {
 
 constexpr int kM = 128;              // features per CTA (TMEM lanes)
 constexpr int kN = 256;              // inputs per tile
-constexpr int kRows = kTailRows;     // reduction per stage
-constexpr int kBox = kMnBoxBytes;    // 64 columns x 64 rows
-constexpr int kSlab = 16 * 128;      // 64 columns x 16 rows
+constexpr int kBlock = kTailRows;    // rows of a whole block; a stage holds one or two
 constexpr int kChunk = 32 * 128;     // staged output: 32 rows x 128 bytes
 constexpr uint16_t kBothCtas = 0x3;
 
@@ -68,8 +66,10 @@ struct Book {
 
 // GROUPS: epilogue groups of four warps, one for each quarter of the lanes; the groups take
 // the output's 128-byte columns in turn.
-template <bool PAIR, int STAGES, int GROUPS>
+// ROWS: the reduction per stage (64 or 128): with 128, half as many loads of twice the size.
+template <bool PAIR, int ROWS, int STAGES, int GROUPS>
 struct Shape {
+    static constexpr int kBox = 128 * ROWS;  // 64 columns of a stage's rows
     static constexpr int kEpiWarps = 4 * GROUPS;
     static constexpr int kThreads = 64 + 32 * kEpiWarps;
     static constexpr int kABytes = 2 * kBox;
@@ -81,13 +81,17 @@ struct Shape {
     static_assert(sizeof(Book<STAGES>) <= 1024, "bookkeeping reserve");
 };
 
-template <bool PAIR, bool F32, int STAGES, int GROUPS>
-__global__ void __launch_bounds__(Shape<PAIR, STAGES, GROUPS>::kThreads, 1)
+template <bool PAIR, bool F32, int ROWS, int STAGES, int GROUPS>
+__global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1)
     linear_wgrad_kernel(const __grid_constant__ CUtensorMap tmZ,
                         const __grid_constant__ CUtensorMap tmX,
+                        const __grid_constant__ CUtensorMap tmZ1,
+                        const __grid_constant__ CUtensorMap tmX1,
                         const __grid_constant__ CUtensorMap tmZt,
-                        const __grid_constant__ CUtensorMap tmXt, const Args args) {
-    using S = Shape<PAIR, STAGES, GROUPS>;
+                        const __grid_constant__ CUtensorMap tmXt,
+                        const __grid_constant__ CUtensorMap tmZs,
+                        const __grid_constant__ CUtensorMap tmXs, const Args args) {
+    using S = Shape<PAIR, ROWS, STAGES, GROUPS>;
     constexpr int kCtas = PAIR ? 2 : 1;
     constexpr uint32_t kIdesc = idesc_bf16_f32_major(kM * kCtas, kN, true, true);
     constexpr uint32_t kTmemCols = 2 * kN;
@@ -117,8 +121,14 @@ __global__ void __launch_bounds__(Shape<PAIR, STAGES, GROUPS>::kThreads, 1)
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmZ);
         tma_prefetch_desc(&tmX);
+        if (ROWS > kBlock) {
+            tma_prefetch_desc(&tmZ1);
+            tma_prefetch_desc(&tmX1);
+        }
         tma_prefetch_desc(&tmZt);
         tma_prefetch_desc(&tmXt);
+        tma_prefetch_desc(&tmZs);
+        tma_prefetch_desc(&tmXs);
     }
     if (warp == 1) {
         if (PAIR)
@@ -158,7 +168,7 @@ __global__ void __launch_bounds__(Shape<PAIR, STAGES, GROUPS>::kThreads, 1)
                 tile_of(tile, e, m0, n0, row0, n);
                 const int mc = m0 + rank * kM;
                 const int nc = n0 + rank * (S::kBBoxes * 64);
-                for (int r = 0; r < n; r += kRows) {
+                for (int r = 0; r < n; r += ROWS) {
                     if (!mbar_wait_asleep(&bk.empty[stage], phase ^ 1u, abort_flag,
                                            args.status)) {
                         ok = false;
@@ -166,10 +176,7 @@ __global__ void __launch_bounds__(Shape<PAIR, STAGES, GROUPS>::kThreads, 1)
                     }
                     uint8_t* z = smem + stage * S::kStageBytes;
                     uint8_t* x = z + S::kABytes;
-                    const bool whole = n - r >= kRows;
-                    const int slabs = whole ? 1 : (n - r + 15) / 16;
-                    const uint32_t bytes =
-                        static_cast<uint32_t>((2 + S::kBBoxes) * (whole ? kBox : slabs * kSlab));
+                    const int left = n - r < ROWS ? n - r : ROWS;
                     auto load = [&](const CUtensorMap* map, uint8_t* dst, int c, int row) {
                         if (PAIR)
                             tma_load_2d_pair(map, map_to_cta(smem_u32(&bk.full[stage]), 0), dst, c,
@@ -177,22 +184,31 @@ __global__ void __launch_bounds__(Shape<PAIR, STAGES, GROUPS>::kThreads, 1)
                         else
                             tma_load_2d(map, &bk.full[stage], dst, c, row);
                     };
-                    if (leader) mbar_arrive_expect_tx(&bk.full[stage], kCtas * bytes);
-                    if (whole) {
+                    // rows row .. of both operands, to the stage's row `at`
+                    auto rows = [&](const CUtensorMap* mz, const CUtensorMap* mx, int at, int row) {
 #pragma unroll
                         for (int b = 0; b < 2; ++b)
-                            load(&tmZ, z + b * kBox, mc + 64 * b, row0 + r);
+                            load(mz, z + b * S::kBox + at * 128, mc + 64 * b, row);
 #pragma unroll
                         for (int b = 0; b < S::kBBoxes; ++b)
-                            load(&tmX, x + b * kBox, nc + 64 * b, row0 + r);
+                            load(mx, x + b * S::kBox + at * 128, nc + 64 * b, row);
+                    };
+                    // a partial block: its first 16 rows if that is all, else 64 at once
+                    // (what lies behind the zeros is loaded and not multiplied)
+                    const int part = left % kBlock;
+                    const int loaded = left - part + (part == 0 ? 0 : part <= 16 ? 16 : kBlock);
+                    if (leader)
+                        mbar_arrive_expect_tx(
+                            &bk.full[stage],
+                            static_cast<uint32_t>(kCtas * (2 + S::kBBoxes) * 128 * loaded));
+                    if (left == ROWS) {
+                        rows(&tmZ, &tmX, 0, row0 + r);
                     } else {
-                        for (int s = 0; s < slabs; ++s) {
-                            const int row = e * kTailRows + 16 * s;
-                            for (int b = 0; b < 2; ++b)
-                                load(&tmZt, z + b * kBox + s * kSlab, mc + 64 * b, row);
-                            for (int b = 0; b < S::kBBoxes; ++b)
-                                load(&tmXt, x + b * kBox + s * kSlab, nc + 64 * b, row);
-                        }
+                        if (ROWS > kBlock && left >= kBlock) rows(&tmZ1, &tmX1, 0, row0 + r);
+                        if (part > 16)
+                            rows(&tmZt, &tmXt, left - part, e * kTailRows);
+                        else if (part > 0)
+                            rows(&tmZs, &tmXs, left - part, e * kTailRows);
                     }
                     issued = true;
                     pending |= 1u << stage;
@@ -228,16 +244,17 @@ __global__ void __launch_bounds__(Shape<PAIR, STAGES, GROUPS>::kThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kN);
-                for (int r = 0; r < n; r += kRows) {
+                for (int r = 0; r < n; r += ROWS) {
                     if (!mbar_wait_asleep(&bk.full[stage], phase, abort_flag, args.status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t z = smem_u32(smem + stage * S::kStageBytes);
-                    const uint64_t zd = sw128_mn_desc(z), xd = sw128_mn_desc(z + S::kABytes);
+                    const uint64_t zd = sw128_mn_desc(z, S::kBox);
+                    const uint64_t xd = sw128_mn_desc(z + S::kABytes, S::kBox);
                     const int left = n - r;
-                    const int steps = left >= kRows ? kRows / 16 : (left + 15) / 16;
+                    const int steps = left >= ROWS ? ROWS / 16 : (left + 15) / 16;
                     for (int k = 0; k < steps; ++k) {
                         const uint32_t accumulate = (r != 0 || k != 0) ? 1u : 0u;
                         if (PAIR)
@@ -374,20 +391,25 @@ __global__ void __launch_bounds__(Shape<PAIR, STAGES, GROUPS>::kThreads, 1)
     }
 }
 
-template <bool PAIR, bool F32, int STAGES, int GROUPS>
+template <bool PAIR, bool F32, int ROWS, int STAGES, int GROUPS>
 cudaError_t launch_wgrad(const LinearBwdArgs& a) {
     constexpr int kCtas = PAIR ? 2 : 1;
-    constexpr int kSmem = Shape<PAIR, STAGES, GROUPS>::kSmem;
-    constexpr int kThreads = Shape<PAIR, STAGES, GROUPS>::kThreads;
-    auto kern = linear_wgrad_kernel<PAIR, F32, STAGES, GROUPS>;
+    constexpr int kSmem = Shape<PAIR, ROWS, STAGES, GROUPS>::kSmem;
+    constexpr int kThreads = Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads;
+    auto kern = linear_wgrad_kernel<PAIR, F32, ROWS, STAGES, GROUPS>;
     static PerDeviceOnce once;
     if (const cudaError_t err = opt_in_smem(once, kern, kSmem); err != cudaSuccess) return err;
     const void* dz = a.codes ? a.dz : a.dy;
     const uint64_t tails = static_cast<uint64_t>(a.E) * kTailRows;
-    CUtensorMap z, x, zt, xt;
-    if (!encode_bf16_2d(&z, dz, a.rows, a.N, kRows) || !encode_bf16_2d(&x, a.x, a.rows, a.K, kRows) ||
-        !encode_bf16_2d(&zt, a.dz_tail, tails, a.N, 16) ||
-        !encode_bf16_2d(&xt, a.x_tail, tails, a.K, 16))
+    // a stage's rows, one block's; the tails' rows, their first 16
+    CUtensorMap z, x, z1, x1, zt, xt, zs, xs;
+    if (!encode_bf16_2d(&z, dz, a.rows, a.N, ROWS) || !encode_bf16_2d(&x, a.x, a.rows, a.K, ROWS) ||
+        !encode_bf16_2d(&z1, dz, a.rows, a.N, kBlock) ||
+        !encode_bf16_2d(&x1, a.x, a.rows, a.K, kBlock) ||
+        !encode_bf16_2d(&zt, a.dz_tail, tails, a.N, kBlock) ||
+        !encode_bf16_2d(&xt, a.x_tail, tails, a.K, kBlock) ||
+        !encode_bf16_2d(&zs, a.dz_tail, tails, a.N, 16) ||
+        !encode_bf16_2d(&xs, a.x_tail, tails, a.K, 16))
         return cudaErrorInvalidValue;
     Args g{};
     g.offsets = a.offsets;
@@ -402,7 +424,7 @@ cudaError_t launch_wgrad(const LinearBwdArgs& a) {
     const long long tiles = static_cast<long long>(a.E) * g.m_tiles * g.n_tiles;
     const int most = device_sm_count() / kCtas;
     const int units = static_cast<int>(tiles < most ? tiles : most);
-    if (!PAIR) return launch_k(kern, units, kThreads, kSmem, a.stream, z, x, zt, xt, g);
+    if (!PAIR) return launch_k(kern, units, kThreads, kSmem, a.stream, z, x, z1, x1, zt, xt, zs, xs, g);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(units * kCtas);
     cfg.blockDim = dim3(kThreads);
@@ -415,7 +437,7 @@ cudaError_t launch_wgrad(const LinearBwdArgs& a) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, z, x, zt, xt, g);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, z, x, z1, x1, zt, xt, zs, xs, g);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
@@ -431,15 +453,15 @@ cudaError_t launch_typed(const LinearBwdArgs& a) {
         static_cast<long long>(a.E) * ((a.N + 255) / 256) * ((a.K + kN - 1) / kN);
     if (a.rows / a.E >= kPairRowsPerGroup && pair_tiles >= device_sm_count() / 2 &&
         pair_gemm_enabled()) {
-        const cudaError_t err = launch_wgrad<true, F32, 6, 2>(a);
+        const cudaError_t err = launch_wgrad<true, F32, 128, 3, 2>(a);
         if (err == cudaSuccess || err == cudaErrorInvalidValue) return err;
         cudaGetLastError();  // no room for a pair of CTAs: single SMs
     }
     // Short reductions in bf16 are bound by the epilogue: sixteen warps of it (32 rows, as
     // above: 149 us against 169 with eight and four stages).  fp32 has half the values per
     // byte and twice the bytes, where more writers only scatter them (341 against 316 us).
-    if (!F32 && a.rows / a.E < kPairRowsPerGroup) return launch_wgrad<false, F32, 2, 4>(a);
-    return launch_wgrad<false, F32, 4, 2>(a);
+    if (!F32 && a.rows / a.E < kPairRowsPerGroup) return launch_wgrad<false, F32, 64, 2, 4>(a);
+    return launch_wgrad<false, F32, 64, 4, 2>(a);
 }
 
 }  // namespace

@@ -313,12 +313,13 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t saddr) {
 // Shared-memory descriptor of an MN-major operand with 128-byte swizzle: each k is one
 // 128-byte row of 64 consecutive M/N elements (a 64-column x 64-row TMA box holds 64
 // such rows); consecutive 64-element groups of M/N are one box (8 KiB) apart (leading
-// byte offset), 8-row groups of k are 1024 bytes apart (stride byte offset).
+// byte offset), 8-row groups of k are 1024 bytes apart (stride byte offset).  `box`: bytes of
+// a box with another number of rows.
 constexpr uint32_t kMnBoxBytes = 64 * 128;
-__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t box = kMnBoxBytes) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(kMnBoxBytes >> 4) << 16;
+    d |= static_cast<uint64_t>(box >> 4) << 16;
     d |= static_cast<uint64_t>(1024u >> 4) << 32;
     d |= static_cast<uint64_t>(1u) << 46;
     d |= static_cast<uint64_t>(2u) << 61;

@@ -52,7 +52,7 @@ namespace {
 
 constexpr int kBK = 64;                // reduction per stage
 constexpr int kF = 128;                // features per CTA (TMEM lanes)
-constexpr int kTokens = 256;           // most token columns of a tile
+constexpr int kTokens = 256;           // token columns of an accumulator
 constexpr int kABytes = kF * kBK * 2;  // 16 KiB
 constexpr int kRingBytes = 204 * 1024;
 constexpr int kMaxStages = 11;
@@ -70,7 +70,8 @@ constexpr int kVoteBarrier = 1;
 constexpr int kJoinBarrier = 2;
 constexpr uint16_t kBothCtas = 0x3;
 // A split is worth it from this many 64-steps saved per CTA (below, writing and joining
-// the shares costs more), and a share has at least kMinShare of them.
+// the shares costs more), and one more for every 16 token columns to join; a share has at
+// least kMinShare of them, and one more for every 64 columns.
 constexpr int kMinSaved = 8;
 constexpr int kMinShare = 4;
 
@@ -79,6 +80,7 @@ struct Args {
     int E, rows;
     int F;                // output features
     int C;                // reduction length
+    int width;            // most token columns of a tile
     int box;              // token rows per TMA box
     int group;            // token tiles whose rows stay in L2 together
     int act;
@@ -114,6 +116,7 @@ struct Book {
     int tile_start[kMaxExperts + 1];
     int stages, stage_bytes;
     int one_tile_each;                // no group has a second token tile
+    int widest;                       // token columns of the widest tile
 };
 static_assert(sizeof(Book) <= kBookBytes, "bookkeeping reserve");
 
@@ -129,7 +132,8 @@ __device__ __forceinline__ Tile decode_tile(const Book& bk, const Args& a, int f
     while (g + 1 < a.E && tile >= bk.tile_start[g + 1]) ++g;
     const int local = tile - bk.tile_start[g];
     const int row0 = bk.off[g], n = bk.off[g + 1] - row0;
-    const int tt = (n + kTokens - 1) / kTokens;
+    int rest;
+    const int tt = divide(n + a.width - 1, a.width, rest);
     // token tiles in runs of `group`; inside a run feature tiles are outer and token tiles
     // inner, so that CTAs running together share the weights
     int r = local, first = 0, width = tt;
@@ -158,17 +162,17 @@ struct Plan {
     int G, c, num_kb, rounds, rem, share_ctas;
     int pieces;             // of this CTA's share: 0, 1 or 2
     int first, from, to;    // the share: 64-steps from .. to, counted from its first tile
-    __device__ __forceinline__ Plan(int G_, int c_, int total, int num_kb_, bool may_share)
+    __device__ __forceinline__ Plan(int G_, int c_, int total, int num_kb_, int widest, bool may_share)
         : G(G_), c(c_), num_kb(num_kb_) {
         rounds = total / G;
         rem = total - rounds * G;
         share_ctas = pieces = first = from = to = 0;
         if (rem > 0 && may_share) {
             const long long units = static_cast<long long>(rem) * num_kb;
-            long long most = units / kMinShare;
+            long long most = units / (kMinShare + widest / 64);
             if (most > G) most = G;
             // steps saved on the busiest CTA by sharing the last round
-            if (most > rem && num_kb - (units + most - 1) / most >= kMinSaved) {
+            if (most > rem && num_kb - (units + most - 1) / most >= kMinSaved + widest / 16) {
                 share_ctas = static_cast<int>(most);
                 if (c < share_ctas) {
                     const long long u0 = bound(c), u1 = bound(c + 1);
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_group_bounds(args.offsets, args.E, args.rows, bk.off);
         // lane g: group g's token tiles; tile_start is their running sum
         const int n = lane < args.E ? bk.off[lane + 1] - bk.off[lane] : 0;
-        const int tt = (n + kTokens - 1) / kTokens;
+        const int tt = (n + args.width - 1) / args.width;
         int sum = tt;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -287,6 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int fit = kRingBytes / bk.stage_bytes;
             bk.stages = fit < kMaxStages ? fit : kMaxStages;
             bk.one_tile_each = most <= 1;
+            bk.widest = widest;
         }
     }
     tc_fence_before();
@@ -296,7 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const uint32_t tmem_base = bk.tmem_base;
     const int stages = bk.stages, stage_bytes = bk.stage_bytes;
-    const Plan plan(gridDim.x / kCtas, blockIdx.x / kCtas, bk.tile_start[args.E], num_kb, !PAIR);
+    const Plan plan(gridDim.x / kCtas, blockIdx.x / kCtas, bk.tile_start[args.E], num_kb,
+                    bk.widest, !PAIR);
     Pieces<kStep> cur;
     auto next_piece = [&]() { return cur.next(plan, bk, args, ftiles, kTileF); };
 
@@ -622,8 +628,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+int usable_sms() {
+    const int sms = device_sm_count();
+    return sms < kLinearMaxCtas ? sms : kLinearMaxCtas;
+}
+
+// Most tiles of `width` tokens x `features` features there can be.
+long long most_tiles(const LinearArgs& a, int F, int width, int features) {
+    const long long groups = a.rows < a.E ? a.rows : a.E;
+    return (a.rows / width + groups) * ((F + features - 1) / features);
+}
+
 template <bool PAIR, bool TRANSPOSED>
-cudaError_t launch_engine(const LinearArgs& a, int F, int C) {
+cudaError_t launch_engine(const LinearArgs& a, int F, int C, int width) {
     constexpr int kCtas = PAIR ? 2 : 1;
     auto kern = linear_sm100_kernel<PAIR, TRANSPOSED>;
     static PerDeviceOnce once;
@@ -634,6 +651,7 @@ cudaError_t launch_engine(const LinearArgs& a, int F, int C) {
     g.rows = a.rows;
     g.F = F;
     g.C = C;
+    g.width = width;
     // Token tiles of a run: 32 MB of rows, eight at least, so that the tiles in flight cover
     // about as many features as tokens and few of either (8192 x 4096 x 14336, one group,
     // 32 tiles a run: 1263 TFLOP/s, 16: 1372).
@@ -656,16 +674,11 @@ cudaError_t launch_engine(const LinearArgs& a, int F, int C) {
         return cudaErrorInvalidValue;
     for (int b = 0; b < kBoxes && (b == 0 || 16 * b < a.rows); ++b)  // the sizes tiles can have
         if (!encode_bf16_2d(&x.box[b], a.x, a.rows, C, 16 * (b + 1))) return cudaErrorInvalidValue;
-    int sms = device_sm_count();
-    if (sms > kLinearMaxCtas) sms = kLinearMaxCtas;
-    // Most tiles there can be: the groups' token tiles, each with its feature tiles.  A
-    // reduction long enough to be shared can use every SM.
-    const long long ftiles = (F + kF * kCtas - 1) / (kF * kCtas);
-    const long long groups = a.rows < a.E ? a.rows : a.E;
-    const long long tiles = (a.rows / kTokens + groups) * ftiles;
+    // A reduction long enough to be shared can use every SM.
     const long long shares = (C + kBK - 1) / kBK / kMinShare;
-    const long long want = tiles * (shares < 1 ? 1 : shares);
-    const int units = static_cast<int>(want < sms / kCtas ? want : sms / kCtas);
+    const long long want = most_tiles(a, F, width, kF * kCtas) * (shares < 1 ? 1 : shares);
+    const int most = usable_sms() / kCtas;
+    const int units = static_cast<int>(want < most ? want : most);
     if (!PAIR) return launch_k(kern, units, kThreads, kSmemBytes, a.stream, w, x, g);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(units * kCtas);
@@ -683,20 +696,29 @@ cudaError_t launch_engine(const LinearArgs& a, int F, int C) {
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-// Average rows per group from which the products run on pairs of SMs.
+// Average rows per group from which the products run on pairs of SMs, if there is a tile
+// for every pair.
 constexpr int kPairRowsPerGroup = 256;
+constexpr int kMinWidth = 32;
 
 }  // namespace
 
 cudaError_t launch_linear_bf16(const LinearArgs& a, bool transposed) {
-    const int F = a.N, C = a.K;
-    if (a.rows / a.E >= kPairRowsPerGroup && pair_gemm_enabled()) {
-        const cudaError_t err =
-            transposed ? launch_engine<true, true>(a, F, C) : launch_engine<true, false>(a, F, C);
+    const int F = a.N, C = a.K, sms = usable_sms();
+    if (a.rows / a.E >= kPairRowsPerGroup && most_tiles(a, F, kTokens, 2 * kF) >= sms / 2 &&
+        pair_gemm_enabled()) {
+        const cudaError_t err = transposed ? launch_engine<true, true>(a, F, C, kTokens)
+                                           : launch_engine<true, false>(a, F, C, kTokens);
         if (err == cudaSuccess || err == cudaErrorInvalidValue) return err;
         cudaGetLastError();  // no room for a pair of CTAs: single SMs
     }
-    return transposed ? launch_engine<false, true>(a, F, C) : launch_engine<false, false>(a, F, C);
+    // Narrower tiles while there are fewer than SMs: cutting the tokens needs no joining,
+    // cutting the reduction does (616 rows in 4 groups, K = 1688, N = 200: 31.7 us with tiles
+    // of up to 256 tokens, cut into shares)
+    int width = kTokens;
+    while (width > kMinWidth && most_tiles(a, F, width, kF) < sms) width /= 2;
+    return transposed ? launch_engine<false, true>(a, F, C, width)
+                      : launch_engine<false, false>(a, F, C, width);
 }
 
 }  // namespace moe

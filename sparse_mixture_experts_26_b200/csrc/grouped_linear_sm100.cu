@@ -69,11 +69,44 @@ static_assert(kSmemBytes <= 232448, "shared memory");
 constexpr int kVoteBarrier = 1;
 constexpr int kJoinBarrier = 2;
 constexpr uint16_t kBothCtas = 0x3;
-// A split is worth it from this many 64-steps saved per CTA (below, writing and joining
-// the shares costs more), and one more for every 16 token columns to join; a share has at
-// least kMinShare of them, and one more for every 64 columns.
-constexpr int kMinSaved = 8;
-constexpr int kMinShare = 4;
+constexpr int kMinShare = 4;           // 64-steps of a share, at least
+
+// What a CTA's work takes, in clocks; rough, to choose among layouts.  A stage of 128
+// features x `width` tokens: the tensor core's time (two clocks a token; on a pair both
+// halves) or the bytes from L2, 36 a clock and SM for single SMs and 55 for pairs, as
+// measured.  Joining shares: rounds of 32 tokens and four shares, each a memory latency.
+__host__ __device__ inline float stage_clocks(int width, bool pair) {
+    const float tensor = 2.f * width;
+    const float bytes = 16384.f + 128.f * (pair ? width / 2 : width);
+    const float load = bytes / (pair ? 55.f : 36.f);
+    return tensor > load ? tensor : load;
+}
+constexpr float kJoinClocks = 2200.f, kShareClocks = 3000.f;
+
+// How many CTAs (0: none) share the reduction of the last `rem` tiles, and the clocks.
+struct Sharing {
+    int ctas;
+    float clocks;
+    __host__ __device__ Sharing(int rem, int num_kb, int width, int G) {
+        const float stage = stage_clocks(width, false), whole = num_kb * stage;
+        const float join = static_cast<float>((width + 31) / 32) * kJoinClocks;
+        ctas = 0;
+        clocks = whole;
+        // the number of shares a tile where more of them cost as much as they save
+        const int best = static_cast<int>(sqrtf(4.f * whole / join));
+        const long long units = static_cast<long long>(rem) * num_kb;
+        long long most = static_cast<long long>(rem) * (best < 2 ? 2 : best);
+        if (most > units / kMinShare) most = units / kMinShare;
+        if (most > G) most = G;
+        if (rem == 0 || most <= rem) return;
+        const float steps = static_cast<float>((units + most - 1) / most);
+        const float shared =
+            steps * stage + static_cast<float>(most / rem / 4 + 1) * join + kShareClocks;
+        if (shared >= whole) return;
+        ctas = static_cast<int>(most);
+        clocks = shared;
+    }
+};
 
 struct Args {
     const int32_t* offsets;
@@ -168,19 +201,13 @@ struct Plan {
         rem = total - rounds * G;
         share_ctas = pieces = first = from = to = 0;
         if (rem > 0 && may_share) {
-            const long long units = static_cast<long long>(rem) * num_kb;
-            long long most = units / (kMinShare + widest / 64);
-            if (most > G) most = G;
-            // steps saved on the busiest CTA by sharing the last round
-            if (most > rem && num_kb - (units + most - 1) / most >= kMinSaved + widest / 16) {
-                share_ctas = static_cast<int>(most);
-                if (c < share_ctas) {
-                    const long long u0 = bound(c), u1 = bound(c + 1);
-                    first = static_cast<int>(u0 / num_kb);
-                    from = static_cast<int>(u0 - static_cast<long long>(first) * num_kb);
-                    to = from + static_cast<int>(u1 - u0);
-                    pieces = to > num_kb ? 2 : 1;
-                }
+            share_ctas = Sharing(rem, num_kb, widest, G).ctas;
+            if (c < share_ctas) {
+                const long long u0 = bound(c), u1 = bound(c + 1);
+                first = static_cast<int>(u0 / num_kb);
+                from = static_cast<int>(u0 - static_cast<long long>(first) * num_kb);
+                to = from + static_cast<int>(u1 - u0);
+                pieces = to > num_kb ? 2 : 1;
             }
         }
     }
@@ -547,11 +574,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     finish(c0 + my_tok, at, v);
                     at += kEpiGroups * kRound * F;
                 }
-            } else {
+            } else if constexpr (!PAIR) {
                 // a share: the fp32 tile to the workspace as [token][feature]
                 const int rem_tile = tile - plan.rounds * plan.G;
                 float* slot = args.partials +
-                              static_cast<size_t>((plan.c * 2 + i) * kCtas + rank) * slot_floats;
+                              static_cast<size_t>(plan.c * 2 + i) * slot_floats;
                 if (group * kRound >= t.nt) release(acc);
                 for (int c0 = group * kRound; c0 < t.nt; c0 += kEpiGroups * kRound) {
                     uint32_t r[kRound];
@@ -564,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const long long u = static_cast<long long>(rem_tile) * num_kb;
                 const int first = plan.holder(u), last = plan.holder(u + num_kb - 1);
-                uint32_t* counter = args.counters + rem_tile * kCtas + rank;
+                uint32_t* counter = args.counters + rem_tile;
                 __threadfence();
                 sync_epilogue();
                 if (threadIdx.x == 64) {
@@ -575,39 +602,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sync_epilogue();
                 if (bk.last) {
                     __threadfence();
-                    // kJoin tokens a thread at a time, so that enough loads are in flight
-                    constexpr int kJoin = 2;
-                    for (int tok0 = group * kRound * kJoin + my_tok; tok0 < t.nt;
-                         tok0 += kEpiGroups * kRound * kJoin) {
-                        float v[kJoin][8] = {};
-#pragma unroll 2
-                        for (int s = first; s <= last; ++s) {
-                            const int sseg = plan.bound(s) / num_kb == rem_tile ? 0 : 1;
-                            const float4* src = reinterpret_cast<const float4*>(
-                                args.partials +
-                                static_cast<size_t>((s * 2 + sseg) * kCtas + rank) * slot_floats +
-                                tok0 * kF + my_f);
-                            float4 lo[kJoin], hi[kJoin];
-#pragma unroll
-                            for (int k = 0; k < kJoin; ++k) {
-                                if (tok0 + kRound * k >= t.nt) continue;
-                                lo[k] = __ldcg(src + k * (kRound * kF / 4));
-                                hi[k] = __ldcg(src + k * (kRound * kF / 4) + 1);
-                            }
-#pragma unroll
-                            for (int k = 0; k < kJoin; ++k) {
-                                if (tok0 + kRound * k >= t.nt) continue;
-                                v[k][0] += lo[k].x, v[k][1] += lo[k].y;
-                                v[k][2] += lo[k].z, v[k][3] += lo[k].w;
-                                v[k][4] += hi[k].x, v[k][5] += hi[k].y;
-                                v[k][6] += hi[k].z, v[k][7] += hi[k].w;
-                            }
+                    // a share that began in an earlier tile has this one as its second
+                    const size_t stride = 2 * slot_floats;
+                    const float* shares =
+                        args.partials + static_cast<size_t>(first) * stride + my_f;
+                    const size_t second = plan.bound(first) < u ? slot_floats : 0;
+                    for (int tok = group * kRound + my_tok; tok < t.nt;
+                         tok += kEpiGroups * kRound) {
+                        float v[8] = {};
+                        const float* src = shares + tok * kF;
+#pragma unroll 4
+                        for (int s = 0; s <= last - first; ++s) {
+                            const float4* p = reinterpret_cast<const float4*>(
+                                src + s * stride + (s == 0 ? second : 0));
+                            const float4 lo = __ldcg(p), hi = __ldcg(p + 1);
+                            v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
+                            v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
                         }
-                        // unrolled: the sums stay in registers
-#pragma unroll
-                        for (int k = 0; k < kJoin; ++k)
-                            if (tok0 + kRound * k < t.nt)
-                                finish(tok0 + kRound * k, origin + (tok0 + kRound * k) * F, v[k]);
+                        finish(tok, origin + tok * F, v);
                     }
                 }
             }
@@ -627,6 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_dealloc(tmem_base, kTmemCols);
     }
 }
+
+constexpr int kMinWidth = 32;  // narrowest tile limit
 
 int usable_sms() {
     const int sms = device_sm_count();
@@ -696,29 +710,68 @@ cudaError_t launch_engine(const LinearArgs& a, int F, int C, int width) {
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-// Average rows per group from which the products run on pairs of SMs, if there is a tile
-// for every pair.
-constexpr int kPairRowsPerGroup = 256;
-constexpr int kMinWidth = 32;
+struct Layout {
+    bool pair;
+    int width;  // token columns of a tile, at most
+};
+
+// The layout with the least clocks for groups of the average size; the weights' bytes from
+// HBM (23 a clock and SM) are a floor for all, and of layouts at the floor the first wins:
+// single SMs, wide tiles.  Measured (us; pairs, then single SMs with tiles of up to 256, 128,
+// 64 and 32 tokens):
+//   8 groups, 256 rows, K 4096, N 14336       158  149  149  149  186
+//   8 groups, 2048 rows, K 4096, N 14336      227  252  291  448  856
+//   1 group, 256 rows, K 4096, N 14336         33   35   40   62  109
+//   2 groups, 3968 rows, K 11512, N 136        76   57   51   60   86
+//   1 group, 1496 rows, K 5144, N 192          39   49   26   22   26
+//   1 group, 100 rows, K 8192, N 1024          39   36   36   20   20
+Layout choose_layout(const LinearArgs& a, int F, int C) {
+    const int sms = usable_sms();
+    const int groups = a.rows < a.E ? a.rows : a.E;
+    const int n = (a.rows + groups - 1) / groups;
+    const int num_kb = (C + kBK - 1) / kBK;
+    const float floor = 2.f * groups * F * C / (23.f * sms);
+    auto tiles = [&](int width, int features, int step, int& wide) {
+        const int tt = (n + width - 1) / width;
+        wide = ((n + tt - 1) / tt + step - 1) / step * step;
+        return static_cast<long long>(groups) * tt * ((F + features - 1) / features);
+    };
+    Layout best{false, kTokens};
+    float least = 0.f;
+    auto offer = [&](bool pair, int width, float clocks) {
+        if (clocks < floor) clocks = floor;
+        if (least == 0.f || clocks < least) best = {pair, width}, least = clocks;
+    };
+    for (int width = kTokens; width >= kMinWidth; width /= 2) {
+        int wide;
+        const long long all = tiles(width, kF, 16, wide);
+        const int rem = static_cast<int>(all % sms);
+        float clocks = static_cast<float>(all / sms) * num_kb * stage_clocks(wide, false);
+        if (rem > 0) clocks += Sharing(rem, num_kb, wide, sms).clocks;
+        offer(false, width, clocks);
+    }
+    if (pair_gemm_enabled()) {
+        int wide;
+        const long long all = tiles(kTokens, 2 * kF, 32, wide), pairs = sms / 2;
+        offer(true, kTokens,
+              static_cast<float>((all + pairs - 1) / pairs) * num_kb * stage_clocks(wide, true));
+    }
+    return best;
+}
 
 }  // namespace
 
 cudaError_t launch_linear_bf16(const LinearArgs& a, bool transposed) {
-    const int F = a.N, C = a.K, sms = usable_sms();
-    if (a.rows / a.E >= kPairRowsPerGroup && most_tiles(a, F, kTokens, 2 * kF) >= sms / 2 &&
-        pair_gemm_enabled()) {
-        const cudaError_t err = transposed ? launch_engine<true, true>(a, F, C, kTokens)
-                                           : launch_engine<true, false>(a, F, C, kTokens);
+    const int F = a.N, C = a.K;
+    const Layout l = choose_layout(a, F, C);
+    if (l.pair) {
+        const cudaError_t err = transposed ? launch_engine<true, true>(a, F, C, l.width)
+                                           : launch_engine<true, false>(a, F, C, l.width);
         if (err == cudaSuccess || err == cudaErrorInvalidValue) return err;
         cudaGetLastError();  // no room for a pair of CTAs: single SMs
     }
-    // Narrower tiles while there are fewer than SMs: cutting the tokens needs no joining,
-    // cutting the reduction does (616 rows in 4 groups, K = 1688, N = 200: 31.7 us with tiles
-    // of up to 256 tokens, cut into shares)
-    int width = kTokens;
-    while (width > kMinWidth && most_tiles(a, F, width, kF) < sms) width /= 2;
-    return transposed ? launch_engine<false, true>(a, F, C, width)
-                      : launch_engine<false, false>(a, F, C, width);
+    return transposed ? launch_engine<false, true>(a, F, C, l.width)
+                      : launch_engine<false, false>(a, F, C, l.width);
 }
 
 }  // namespace moe

@@ -488,7 +488,17 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// cuTensorMapEncodeTiled is a driver call: it needs a context bound to the calling thread,
+// which a thread without a runtime call of its own yet does not have.
+static void bind_thread_to_device() {
+    static thread_local bool bound = false;
+    if (bound) return;
+    int dev = 0;
+    bound = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+}
+
 static EncodeTiledFn get_encode_fn() {
+    bind_thread_to_device();
     static EncodeTiledFn fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {

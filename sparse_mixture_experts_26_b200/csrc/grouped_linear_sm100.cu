@@ -364,29 +364,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (PAIR) {
                         const uint32_t bar = map_to_cta(smem_u32(&bk.full[stage]), 0);
                         if (leader) mbar_arrive_expect_tx(&bk.full[stage], 2 * bytes);
+                        auto load_w = [&](uint8_t* dst, int c0, int c1) {
+                            if (stream)
+                                tma_load_3d_pair_hint(&tmW, bar, dst, c0, c1, t.e, policy);
+                            else
+                                tma_load_3d_pair(&tmW, bar, dst, c0, c1, t.e);
+                        };
                         if (TRANSPOSED) {
-                            tma_load_3d_pair(&tmW, bar, w, f, c, t.e);
-                            tma_load_3d_pair(&tmW, bar, w + kMnBoxBytes, f + 64, c, t.e);
+                            load_w(w, f, c);
+                            load_w(w + kMnBoxBytes, f + 64, c);
                         } else {
-                            tma_load_3d_pair(&tmW, bar, w, c, f, t.e);
+                            load_w(w, c, f);
                         }
                         tma_load_2d_pair(map0, bar, x, c, x_row);
                     } else {
                         uint64_t* bar = &bk.full[stage];
                         mbar_arrive_expect_tx(bar, bytes);
+                        auto load_w = [&](uint8_t* dst, int c0, int c1) {
+                            if (stream)
+                                tma_load_3d_hint(&tmW, bar, dst, c0, c1, t.e, policy);
+                            else
+                                tma_load_3d(&tmW, bar, dst, c0, c1, t.e);
+                        };
                         if (TRANSPOSED) {
-                            if (stream) {
-                                tma_load_3d_hint(&tmW, bar, w, f, c, t.e, policy);
-                                tma_load_3d_hint(&tmW, bar, w + kMnBoxBytes, f + 64, c, t.e,
-                                                 policy);
-                            } else {
-                                tma_load_3d(&tmW, bar, w, f, c, t.e);
-                                tma_load_3d(&tmW, bar, w + kMnBoxBytes, f + 64, c, t.e);
-                            }
-                        } else if (stream) {
-                            tma_load_3d_hint(&tmW, bar, w, c, f, t.e, policy);
+                            load_w(w, f, c);
+                            load_w(w + kMnBoxBytes, f + 64, c);
                         } else {
-                            tma_load_3d(&tmW, bar, w, c, f, t.e);
+                            load_w(w, c, f);
                         }
                         tma_load_2d(map0, bar, x, c, x_row);
                         if (n1 > 0) tma_load_2d(map1, bar, x + 128 * kBK * 2, c, x_row + 128);

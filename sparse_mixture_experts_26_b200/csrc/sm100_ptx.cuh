@@ -475,6 +475,17 @@ __device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint32_
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d_pair_hint(const CUtensorMap* map,
+                                                      uint32_t bar_cluster_addr, void* dst, int c0,
+                                                      int c1, int c2, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster_addr), "r"(c0), "r"(c1), "r"(c2),
+        "l"(policy)
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(slot)),

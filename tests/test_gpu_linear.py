@@ -17,6 +17,8 @@ SHAPES = [
     ((128, 129, 127), 512, 256), ((257, 1, 300, 0), 192, 328), ((500,), 4104, 136),
     ((700, 13, 0, 311), 264, 520), ((1025,), 64, 72), ((2, 3, 1) * 10 + (4, 0), 128, 96),
     ((1500, 0, 600), 328, 712), ((300, 280, 290, 310), 1032, 640), ((4097,), 200, 264),
+    # reductions cut into many shares, for few tokens and for many
+    ((5, 0, 3), 20000, 40), ((100,), 8192, 264), ((250, 6), 5000, 136), ((1496,), 5144, 192),
 ]
 
 
@@ -455,6 +457,83 @@ def test_two_streams_with_a_workspace_each():
     torch.cuda.synchronize()
     for t, _, y in sets:
         check_y(y, t, counts, K, "gelu", 90)
+
+
+def test_four_threads_call_at_once():
+    """Own streams and workspaces, the first calls of their shapes: equal to serial calls."""
+    import threading
+    jobs = []
+    for i, counts in enumerate([(3, 0, 9), (70, 30, 0), (400, 300, 350), (1, 1, 1)]):
+        t = R.inputs(counts, 264, 648 + 8 * i, bf, 90 + i)
+        n = sum(counts)
+        y = torch.empty(n, t["W"].shape[1], dtype=bf, device="cuda")
+        dW = torch.empty_like(t["W"])
+        ws = moe.alloc_grouped_linear_workspace(n, 264, y.shape[1], 3)
+        bws = moe.alloc_grouped_linear_backward_workspace(n, 264, y.shape[1], 3)
+        jobs.append((t, R.offsets_of(counts), y, dW, ws, bws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(t, off, y, dW, ws, bws, stream):
+        try:
+            for _ in range(5):
+                moe.moe_grouped_linear(t["x"], off, t["W"], y, ws, bias=t["bias"], act="gelu",
+                                       stream=stream)
+                moe.moe_grouped_linear_backward(t["dy"], t["x"], off, t["W"], bws, dW=dW,
+                                                stream=stream)
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for t, off, y, dW, ws, bws, _ in jobs:
+        y2, dW2 = torch.empty_like(y), torch.empty_like(dW)
+        moe.moe_grouped_linear(t["x"], off, t["W"], y2, ws, bias=t["bias"], act="gelu")
+        moe.moe_grouped_linear_backward(t["dy"], t["x"], off, t["W"], bws, dW=dW2)
+        assert torch.equal(y, y2) and torch.equal(dW, dW2)
+
+
+def test_offsets_beyond_32_bits():
+    """rows x N above 2^31 elements: the last rows and gradients come from their own data."""
+    rows, K, N = 150_016, 64, 14336
+    assert rows * N > 2 ** 31
+    counts = (rows - 3000, 3000)
+    t = R.inputs((1,) * 2, K, N, bf, 5, bias=True)  # W and bias for two groups
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(rows, K, generator=g, device="cuda").to(bf)
+    off = R.offsets_of(counts)
+    ws = moe.alloc_grouped_linear_workspace(rows, K, N, 2)
+    y = torch.empty(rows, N, dtype=bf, device="cuda")
+    codes, scales = moe.alloc_checkpoint(rows, N)
+    moe.moe_grouped_linear_train(x, off, t["W"], y, codes, scales, ws, bias=t["bias"], act="silu")
+    last = slice(rows - 40, rows)
+    z = x[last].double() @ t["W"][1].double().t() + t["bias"][1].double()
+    assert R.relative(y[last], R.act(z, "silu")) <= R.U_BF16
+    kept = R.values(codes[last], scales[last])
+    assert bool(((kept - z).abs() <= R.half_step(scales[last], N) * 1.001 + 1e-4).all())
+    del ws
+    out = torch.empty_like(y)
+    moe.moe_checkpoint_restore(codes, scales, out)
+    assert R.relative(out[last], kept) <= R.U_BF16
+    again = torch.zeros(rows, N, dtype=torch.int8, device="cuda")
+    moe.moe_checkpoint_save(out, again, scales.clone())
+    assert torch.equal(again[last], R.quantise(out[last])[0])
+    del again, out
+    bws = moe.alloc_grouped_linear_backward_workspace(rows, K, N, 2)
+    dx, dW = torch.empty_like(x), torch.empty_like(t["W"])
+    db = torch.empty(2, N, device="cuda")
+    moe.moe_grouped_linear_backward(y, x, off, t["W"], bws, dx=dx, dW=dW, db=db, codes=codes,
+                                    scales=scales, act="silu")
+    r = slice(rows - 3000, rows)
+    dz = y[r].double() * R.slope(R.values(codes[r], scales[r]), "silu")
+    assert R.relative(dx[r], dz @ t["W"][1].double()) <= 2 * R.U_BF16
+    assert R.relative(dW[1], dz.t() @ x[r].double()) <= 2 * R.U_BF16
+    assert R.relative(db[1], dz.sum(0)) <= 2.0 ** -15
 
 
 def test_one_workspace_serves_smaller_batches():

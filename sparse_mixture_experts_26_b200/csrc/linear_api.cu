@@ -60,8 +60,11 @@ T* at(void* ws, size_t off) {
     return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
-// Short calls overlap the launch of one kernel with the end of the one before (PdlScope).
-bool short_call(int rows) { return rows <= 256; }
+// Short calls overlap the launch of one kernel with the end of the one before (PdlScope):
+// 637 x 2 rows, K = 104, N = 5328, backward 49.7 -> 42.6 us.  Long ones gain nothing.
+bool short_call(int rows, int K, int N) {
+    return rows <= 256 || static_cast<double>(rows) * K * N < 8e9;
+}
 
 moe_status finish_linear(cudaError_t err, cudaStream_t s, uint32_t* status) {
     if (err == cudaErrorInvalidValue) return MOE_ERR_INVALID_ARG;  // tensor map refused
@@ -98,7 +101,7 @@ moe_status linear_impl(const char* name, bool train, const void* x, const int32_
     const LinearWs L = linear_ws(rows, K, N, E, dt, false);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
     Range range(name);
-    PdlScope pdl(short_call(rows));
+    PdlScope pdl(short_call(rows, K, N));
     LinearArgs a{};
     a.x = x;
     a.offsets = offsets;
@@ -157,7 +160,7 @@ moe_status moe_checkpoint_save(const void* v, int rows, int N, moe_dtype dt, int
     if (st != MOE_OK) return st;
     if (rows == 0) return MOE_OK;
     if (!ptrs_ok({v, codes, scales})) return MOE_ERR_INVALID_ARG;
-    PdlScope pdl(short_call(rows));
+    PdlScope pdl(short_call(rows, 8, N));
     return finish_linear(launch_checkpoint_save(v, rows, N, dt, codes, scales, stream), stream,
                          nullptr);
 }
@@ -169,7 +172,7 @@ moe_status moe_checkpoint_restore(const int8_t* codes, const float* scales, int 
     if (!valid_act(act)) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
     if (!ptrs_ok({codes, scales, out})) return MOE_ERR_INVALID_ARG;
-    PdlScope pdl(short_call(rows));
+    PdlScope pdl(short_call(rows, 8, N));
     return finish_linear(
         launch_checkpoint_restore(codes, scales, rows, N, act, out_dt, out, stream), stream,
         nullptr);
@@ -205,7 +208,7 @@ moe_status moe_grouped_linear_backward(const void* dy, const void* x, const int3
     const LinearWs L = linear_ws(rows, K, N, E, dt, true);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
     Range range("moe_grouped_linear_backward");
-    PdlScope pdl(short_call(rows));
+    PdlScope pdl(short_call(rows, K, N));
     LinearBwdArgs a{};
     a.dy = dy;
     a.x = x;

@@ -524,54 +524,74 @@ def alloc_checkpoint(rows: int, N: int, device="cuda"):
             torch.empty(rows, nb, dtype=torch.float32, device=device))
 
 
+# The checks below cost as much as a small kernel, so each compares in place and calls
+# _expect, which words the error, only when it fails.
 def _check_checkpoint(codes, scales, rows: int, N: int) -> None:
-    _expect("codes", codes, (rows, N), torch.int8)
-    _expect("scales", scales, (rows, (N + CHECKPOINT_BLOCK - 1) // CHECKPOINT_BLOCK),
-            torch.float32)
+    if codes.shape != (rows, N) or codes.dtype != torch.int8:
+        _expect("codes", codes, (rows, N), torch.int8)
+    nb = (N + CHECKPOINT_BLOCK - 1) // CHECKPOINT_BLOCK
+    if scales.shape != (rows, nb) or scales.dtype != torch.float32:
+        _expect("scales", scales, (rows, nb), torch.float32)
 
 
 def _call(fn: str, tensors, stream, *args) -> None:
-    """Call ``fn(*args, stream)`` under the tensors' device.  Small batches spend their time
-    here, so the device is switched only if another one is current, and the current stream
-    is read as a bare handle."""
-    dev = _dev(*[t for t in tensors if t is not None])
-    if torch.cuda.current_device() == dev.index:
-        handle = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None
-                  else _stream(stream))
-        _check(fn, getattr(_lib, fn)(*args, handle))
+    """Call ``fn(*args, stream)`` under the tensors' device: switched only if another one is
+    current, and the current stream read as a bare handle."""
+    first = tensors[0]
+    index = first.get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != index or index < 0 or not t.is_contiguous()):
+            _dev(*[t for t in tensors if t is not None])  # says what is wrong
+    f = getattr(_lib, fn)
+    if torch.cuda.current_device() == index:
+        code = f(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None
+                 else _stream(stream))
     else:
-        with torch.cuda.device(dev):
-            _check(fn, getattr(_lib, fn)(*args, _stream(stream)))
+        with torch.cuda.device(index):
+            code = f(*args, _stream(stream))
+    if code:
+        _check(fn, code)
+
+
+_DTYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
 
 
 def _linear_dims(x, offsets, W, bias):
     if x.dim() != 2 or W.dim() != 3:
         raise ValueError("x must be [rows, K] and W [E, N, K]")
     rows, K = x.shape
-    E, N, _ = W.shape
-    dt = _dt(x)
-    _expect("W", W, (E, N, K), x.dtype)
+    E, N, K_w = W.shape
+    dtype = x.dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        _dt(x)
+    if K_w != K or W.dtype != dtype:
+        _expect("W", W, (E, N, K), dtype)
     if offsets is None:
         if E != 1:
             raise ValueError("offsets may be None only with one expert")
-    else:
+    elif offsets.numel() != E + 1 or offsets.dtype != torch.int32:
         _expect_numel("offsets", offsets, E + 1, torch.int32)
-    if bias is not None:
-        _expect("bias", bias, (E, N), x.dtype)
+    if bias is not None and (bias.shape != (E, N) or bias.dtype != dtype):
+        _expect("bias", bias, (E, N), dtype)
     return rows, K, N, E, dt
 
 
 def _linear(fn, x, offsets, W, y, ws, bias, residual, act, codes, scales, stream) -> None:
     rows, K, N, E, dt = _linear_dims(x, offsets, W, bias)
-    _expect("y", y, (rows, N))
-    y_dt = _dt(y)
-    if residual is not None:
+    if y.shape != (rows, N):
+        _expect("y", y, (rows, N))
+    y_dt = _DTYPES.get(y.dtype)
+    if y_dt is None:
+        _dt(y)
+    if residual is not None and (residual.shape != (rows, N) or residual.dtype != x.dtype):
         _expect("residual", residual, (rows, N), x.dtype)
     _ws("ws", ws)
-    kept = () if codes is None else (_ptr(codes), _ptr(scales))
+    kept = () if codes is None else (codes.data_ptr(), scales.data_ptr())
     _call(fn, (x, offsets, W, y, ws, bias, residual, codes, scales), stream,
-          _ptr(x), _ptr(offsets), _ptr(W), _ptr(bias), _ptr(residual), rows, K, N, E, _act(act),
-          dt, y_dt, _ptr(y), *kept, _ptr(ws), ws.numel())
+          x.data_ptr(), _ptr(offsets), W.data_ptr(), _ptr(bias), _ptr(residual), rows, K, N, E,
+          _ACTS[act] if act in _ACTS else _act(act), dt, y_dt, y.data_ptr(), *kept,
+          ws.data_ptr(), ws.numel())
 
 
 def moe_grouped_linear(x, offsets, W, y, ws, bias=None, residual=None, act: str = "none",
@@ -631,14 +651,16 @@ def moe_grouped_linear_backward(dy, x, offsets, W, ws, dx=None, dW=None, db=None
     (x's dtype), ``dW`` (bf16 or fp32) and ``db`` (fp32) that is given is overwritten.
     ``codes`` and ``scales`` may be left out with ``act="none"``."""
     rows, K, N, E, dt = _linear_dims(x, offsets, W, None)
-    _expect("dy", dy, (rows, N), x.dtype)
-    if dx is not None:
+    if dy.shape != (rows, N) or dy.dtype != x.dtype:
+        _expect("dy", dy, (rows, N), x.dtype)
+    if dx is not None and (dx.shape != (rows, K) or dx.dtype != x.dtype):
         _expect("dx", dx, (rows, K), x.dtype)
     dw_dt = dt
     if dW is not None:
-        _expect("dW", dW, (E, N, K))
+        if dW.shape != W.shape:
+            _expect("dW", dW, (E, N, K))
         dw_dt = _dt(dW)
-    if db is not None:
+    if db is not None and (db.shape != (E, N) or db.dtype != torch.float32):
         _expect("db", db, (E, N), torch.float32)
     if (codes is None) != (scales is None):
         raise ValueError("codes and scales go together")

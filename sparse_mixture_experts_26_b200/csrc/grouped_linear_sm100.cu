@@ -81,29 +81,33 @@ __host__ __device__ inline float stage_clocks(int width, bool pair) {
     const float load = bytes / (pair ? 55.f : 36.f);
     return tensor > load ? tensor : load;
 }
-constexpr float kJoinClocks = 2200.f, kShareClocks = 3000.f;
+// Pairs: a cluster's launch and its two synchronisations, without programmatic launch.
+constexpr float kJoinClocks = 2200.f, kShareClocks = 3000.f, kPairClocks = 3000.f;
 
-// How many CTAs (0: none) share the reduction of the last `rem` tiles, and the clocks.
+// How many CTAs (0: none) share the reduction of the last `rem` tiles, and the clocks.  No
+// integer division: every thread goes through this before its first piece of work.
+constexpr int kMostSteps = 1 << 15;  // of a shared reduction: 160 x 160 of them fit 32 bits
 struct Sharing {
     int ctas;
     float clocks;
     __host__ __device__ Sharing(int rem, int num_kb, int width, int G) {
         const float stage = stage_clocks(width, false), whole = num_kb * stage;
-        const float join = static_cast<float>((width + 31) / 32) * kJoinClocks;
         ctas = 0;
         clocks = whole;
+        if (rem == 0 || num_kb < 2 * kMinShare || num_kb >= kMostSteps) return;
+        const float join = static_cast<float>((width + 31) / 32) * kJoinClocks;
         // the number of shares a tile where more of them cost as much as they save
         const int best = static_cast<int>(sqrtf(4.f * whole / join));
-        const long long units = static_cast<long long>(rem) * num_kb;
-        long long most = static_cast<long long>(rem) * (best < 2 ? 2 : best);
-        if (most > units / kMinShare) most = units / kMinShare;
+        int most = rem * (best < 2 ? 2 : best);
+        if (most > rem * num_kb / kMinShare) most = rem * num_kb / kMinShare;
         if (most > G) most = G;
-        if (rem == 0 || most <= rem) return;
-        const float steps = static_cast<float>((units + most - 1) / most);
-        const float shared =
-            steps * stage + static_cast<float>(most / rem / 4 + 1) * join + kShareClocks;
+        if (most <= rem) return;
+        const float each = static_cast<float>(most) / static_cast<float>(rem);  // shares a tile
+        const float shared = (num_kb / each + 1.f) * stage +
+                             static_cast<float>(static_cast<int>(each) / 4 + 1) * join +
+                             kShareClocks;
         if (shared >= whole) return;
-        ctas = static_cast<int>(most);
+        ctas = most;
         clocks = shared;
     }
 };
@@ -197,22 +201,21 @@ struct Plan {
     int first, from, to;    // the share: 64-steps from .. to, counted from its first tile
     __device__ __forceinline__ Plan(int G_, int c_, int total, int num_kb_, int widest, bool may_share)
         : G(G_), c(c_), num_kb(num_kb_) {
-        rounds = total / G;
-        rem = total - rounds * G;
+        rounds = divide(total, G, rem);
         share_ctas = pieces = first = from = to = 0;
         if (rem > 0 && may_share) {
             share_ctas = Sharing(rem, num_kb, widest, G).ctas;
             if (c < share_ctas) {
-                const long long u0 = bound(c), u1 = bound(c + 1);
-                first = static_cast<int>(u0 / num_kb);
-                from = static_cast<int>(u0 - static_cast<long long>(first) * num_kb);
-                to = from + static_cast<int>(u1 - u0);
+                const int u0 = bound(c), u1 = bound(c + 1);
+                first = divide(u0, num_kb, from);
+                to = from + u1 - u0;
                 pieces = to > num_kb ? 2 : 1;
             }
         }
     }
-    __device__ __forceinline__ long long bound(int i) const {  // first 64-step of share i
-        return static_cast<long long>(i) * rem * num_kb / share_ctas;
+    __device__ __forceinline__ int bound(int i) const {  // first 64-step of share i
+        int rest;
+        return divide(i * rem * num_kb, share_ctas, rest);
     }
     // Piece i of this CTA's work; false when there is none.
     __device__ __forceinline__ bool get(int i, int& tile, int& kb0, int& kb1) const {
@@ -229,8 +232,8 @@ struct Plan {
         return i < rounds || (i == rounds && share_ctas == 0 && c < rem);
     }
     // The share that holds the remaining tiles' 64-step u.
-    __device__ __forceinline__ int holder(long long u) const {
-        int i = static_cast<int>(u * share_ctas / (static_cast<long long>(rem) * num_kb));
+    __device__ __forceinline__ int holder(int u) const {
+        int rest, i = divide(u * share_ctas, rem * num_kb, rest);
         while (i + 1 < share_ctas && bound(i + 1) <= u) ++i;
         while (i > 0 && bound(i) > u) --i;
         return i;
@@ -593,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < kRound; ++k)
                         __stcg(slot + (c0 + k) * kF + q * 32 + lane, bits_f32(r[k]));
                 }
-                const long long u = static_cast<long long>(rem_tile) * num_kb;
+                const int u = rem_tile * num_kb;
                 const int first = plan.holder(u), last = plan.holder(u + num_kb - 1);
                 uint32_t* counter = args.counters + rem_tile;
                 __threadfence();
@@ -758,7 +761,8 @@ Layout choose_layout(const LinearArgs& a, int F, int C) {
         int wide;
         const long long all = tiles(kTokens, 2 * kF, 32, wide), pairs = sms / 2;
         offer(true, kTokens,
-              static_cast<float>((all + pairs - 1) / pairs) * num_kb * stage_clocks(wide, true));
+              static_cast<float>((all + pairs - 1) / pairs) * num_kb * stage_clocks(wide, true) +
+                  kPairClocks);
     }
     return best;
 }

@@ -33,7 +33,7 @@ bool optional_ok(const void* p) { return aligned16(p); }  // null is aligned
 
 // Workspace regions (1 KiB aligned): status word, counters.
 struct LinearWs {
-    size_t status, counters, partials, dz, dz_tail, x_tail, db_part, total;
+    size_t status, counters, partials, dz, dz_tail, x_tail, db_part, db_counters, total;
 };
 LinearWs linear_ws(int rows, int K, int N, int E, moe_dtype dt, bool backward) {
     LinearWs L{};
@@ -51,6 +51,7 @@ LinearWs linear_ws(int rows, int K, int N, int E, moe_dtype dt, bool backward) {
     L.dz_tail = take(tail * N * 2);
     L.x_tail = take(tail * K * 2);
     L.db_part = take(b * linear_chunks(rows, E) * N * 4);
+    L.db_counters = take(b * linear_db_counters(N, E) * 4);
     L.total = o;
     return L;
 }
@@ -229,6 +230,7 @@ moe_status moe_grouped_linear_backward(const void* dy, const void* x, const int3
     a.dz_tail = at<void>(ws, L.dz_tail);
     a.x_tail = at<void>(ws, L.x_tail);
     a.db_part = at<float>(ws, L.db_part);
+    a.db_counters = at<uint32_t>(ws, L.db_counters);
     a.status = at<uint32_t>(ws, L.status);
     a.counters = at<uint32_t>(ws, L.counters);
     a.partials = at<float>(ws, L.partials);

@@ -7,12 +7,14 @@
 // hold anything; this way they are never read as part of a sum.
 //
 // Bytes: dy 2, code 1.125, dz 2 per value; 25 instructions a value (GELU) weigh as much.  A
-// block takes 256 columns of a chunk of up to 64 rows of one group: a warp reads 512 bytes of
+// block takes 256 columns of a chunk of 64 to 512 rows of one group: a warp reads 512 bytes of
 // a row, eight columns a lane, and the eight warps take the rows in turn, two in flight a
-// thread.  The warps' column sums are added in order in shared memory, the chunks' by a
-// second launch.  Without an activation dz is dy itself: only the tails and db are made.
-// Measured at 8192 x 14336 with db (us; 600 MB): ReLU 113, SiLU 127, GELU 146; four rows in
-// flight at three blocks an SM 124, 135 and 151.
+// thread.  The warps' column sums are added in order in shared memory; the chunks' go to the
+// workspace, and the block that brings a group's last chunk adds them in chunk order
+// (whichever block that is, so db does not depend on the timing).  Without an activation dz
+// is dy itself: only the tails and db are made.
+// Measured at 8192 x 14336 with db (us; 600 MB): ReLU 119, SiLU 128, GELU 139; with chunks of
+// 64 rows 131, 142 and 160.
 #include <cuda_bf16.h>
 
 #include "linear_device.cuh"
@@ -35,30 +37,37 @@ struct DzArgs {
     __nv_bfloat16* dz;
     __nv_bfloat16* dz_tail;  // nullptr: no tails wanted
     __nv_bfloat16* x_tail;
-    float* sums;           // db itself or the chunk sums; nullptr: not wanted
-    bool by_group;         // every group has at most one chunk: chunk e is group e
+    float* db;             // nullptr: not wanted
+    float* part;           // the chunk sums of groups with several
+    uint32_t* counters;    // one for each group and strip, zero between calls
     int items;             // chunks times strips
+    int chunk_rows;        // a multiple of kTailRows
     int strips;            // column strips of a chunk: the first n_strips of dz, then of x
     int n_strips;
 };
 
 // One chunk's strip of columns.  All threads of the block call this together.
 __device__ __forceinline__ void dz_item(const DzArgs& a, const int* off, float (*s_sum)[kCols],
-                                        int item) {
+                                        int& s_last, int item) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int strip;
     const int chunk = divide(item, a.strips, strip);
-    int e = 0, i = chunk;  // chunk i of group e
+    int e = 0, i = chunk, chunks = 0;  // chunk i of group e's; an empty group has one too
     for (; e < a.E; ++e) {
-        const int chunks = a.by_group ? 1 : (off[e + 1] - off[e] + kTailRows - 1) / kTailRows;
+        int rest;
+        chunks = max(divide(off[e + 1] - off[e] + a.chunk_rows - 1, a.chunk_rows, rest), 1);
         if (i < chunks) break;
         i -= chunks;
     }
     if (e == a.E) return;
-    const int row0 = off[e] + i * kTailRows;
-    const int n = min(off[e + 1] - row0, kTailRows);
-    const bool tail = n > 0 && n < kTailRows && a.dz_tail != nullptr;
-    const int n16 = (n + 15) & ~15;
+    const int of_group = off[e + 1] - off[e];
+    const int first = i * a.chunk_rows;             // this chunk's rows, counted in the group
+    const int end = min(first + a.chunk_rows, of_group);
+    const int row0 = off[e];
+    // the group's last, partial block of 64 rows, if it is in this chunk
+    const int whole = of_group / kTailRows * kTailRows;
+    const bool tail = a.dz_tail != nullptr && end == of_group && whole < of_group;
+    const int end16 = whole + (of_group - whole + 15) / 16 * 16;  // zero rows up to here
     const size_t trow = static_cast<size_t>(e) * kTailRows;
     const float zero[8] = {};
 
@@ -66,28 +75,28 @@ __device__ __forceinline__ void dz_item(const DzArgs& a, const int* off, float (
         const int c = (strip - a.n_strips) * kCols + lane * 8;
         if (!tail || c >= a.K) return;
 #pragma unroll 4
-        for (int r = warp; r < n16; r += kWarps) {
+        for (int r = whole + warp; r < end16; r += kWarps) {
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (r < n)
+            if (r < end)
                 v = *reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(row0 + r) * a.K + c);
-            *reinterpret_cast<uint4*>(a.x_tail + (trow + r) * a.K + c) = v;
+            *reinterpret_cast<uint4*>(a.x_tail + (trow + r - whole) * a.K + c) = v;
         }
         return;
     }
     const int c = strip * kCols + lane * 8;
-    const bool have = c < a.N && (a.codes || a.sums || tail);  // else nothing to do here
+    const bool have = c < a.N && (a.codes || a.db || tail);  // else nothing to do here
     const int nb = ckpt_blocks(a.N);
     float sum[8] = {};
     if (have) {
         constexpr int kFlight = 2;  // rows whose loads are in flight together
-        for (int r0 = warp; r0 < n; r0 += kFlight * kWarps) {
+        for (int r0 = first + warp; r0 < end; r0 += kFlight * kWarps) {
             uint4 dy[kFlight];
             uint2 q[kFlight];
             float s[kFlight];
 #pragma unroll
             for (int k = 0; k < kFlight; ++k) {
                 const int r = r0 + k * kWarps;
-                if (r >= n) continue;
+                if (r >= end) continue;
                 const size_t row = static_cast<size_t>(row0 + r), at = row * a.N + c;
                 dy[k] = *reinterpret_cast<const uint4*>(a.dy + at);
                 if (a.codes) {
@@ -98,7 +107,7 @@ __device__ __forceinline__ void dz_item(const DzArgs& a, const int* off, float (
 #pragma unroll
             for (int k = 0; k < kFlight; ++k) {
                 const int r = r0 + k * kWarps;
-                if (r >= n) continue;
+                if (r >= end) continue;
                 float g[8] = {bf16_lo(dy[k].x), bf16_hi(dy[k].x), bf16_lo(dy[k].y),
                               bf16_hi(dy[k].y), bf16_lo(dy[k].z), bf16_hi(dy[k].z),
                               bf16_lo(dy[k].w), bf16_hi(dy[k].w)};
@@ -110,70 +119,67 @@ __device__ __forceinline__ void dz_item(const DzArgs& a, const int* off, float (
                 }
 #pragma unroll
                 for (int u = 0; u < 8; ++u) sum[u] += g[u];
-                if (tail) store8(a.dz_tail + (trow + r) * a.N + c, g);
+                if (tail && r >= whole) store8(a.dz_tail + (trow + r - whole) * a.N + c, g);
             }
         }
         if (tail)
-            for (int r = n + warp; r < n16; r += kWarps)
-                store8(a.dz_tail + (trow + r) * a.N + c, zero);
+            for (int r = end + warp; r < end16; r += kWarps)
+                store8(a.dz_tail + (trow + r - whole) * a.N + c, zero);
     }
-    if (a.sums == nullptr) return;
-    __syncthreads();  // the last item's sums have been read
-    store8(&s_sum[warp][lane * 8], sum);
-    __syncthreads();
+    if (a.db == nullptr) return;
     const int col = strip * kCols + threadIdx.x;
-    if (col >= a.N) return;
-    float total = s_sum[0][threadIdx.x];
+    // the warps' sums of this thread's column, in order
+    auto join = [&]() {
+        __syncthreads();  // what was there before has been read
+        store8(&s_sum[warp][lane * 8], sum);
+        __syncthreads();
+        float total = s_sum[0][threadIdx.x];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) total += s_sum[w][threadIdx.x];
-    a.sums[static_cast<size_t>(chunk) * a.N + col] = total;
+        for (int w = 1; w < kWarps; ++w) total += s_sum[w][threadIdx.x];
+        return total;
+    };
+    float total = join();
+    float* db = a.db + static_cast<size_t>(e) * a.N + col;
+    if (chunks == 1) {
+        if (col < a.N) *db = total;
+        return;
+    }
+    if (col < a.N) __stcg(a.part + static_cast<size_t>(chunk) * a.N + col, total);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        uint32_t* counter = a.counters + static_cast<size_t>(e) * a.n_strips + strip;
+        s_last = atomicAdd(counter, 1u) == static_cast<uint32_t>(chunks - 1);
+        if (s_last) *counter = 0;  // zero again for the next call
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    // warp w adds chunks w, w + 8, .. of the group, then the warps' sums are added
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[k] = 0.f;
+    if (c < a.N) {
+        const float* part = a.part + static_cast<size_t>(chunk - i) * a.N + c;
+#pragma unroll 4
+        for (int k = warp; k < chunks; k += kWarps) {
+            const float4* p = reinterpret_cast<const float4*>(part + static_cast<size_t>(k) * a.N);
+            const float4 lo = __ldcg(p), hi = __ldcg(p + 1);
+            sum[0] += lo.x, sum[1] += lo.y, sum[2] += lo.z, sum[3] += lo.w;
+            sum[4] += hi.x, sum[5] += hi.y, sum[6] += hi.z, sum[7] += hi.w;
+        }
+    }
+    total = join();
+    if (col < a.N) *db = total;
 }
 
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) linear_dz_kernel(const DzArgs a) {
-    __shared__ int off[kMaxExperts + 1];
+    __shared__ int off[kMaxExperts + 1], s_last;
     __shared__ __align__(16) float s_sum[kWarps][kCols];  // written 16 bytes at a time
     pdl_wait();
     pdl_launch_dependents();
     if (threadIdx.x < 32) load_group_bounds(a.offsets, a.E, a.rows, off);
     __syncthreads();
-    for (int item = blockIdx.x; item < a.items; item += gridDim.x) dz_item(a, off, s_sum, item);
-}
-
-// db[e] = the chunk sums of group e in chunk order: slice s of 8 adds chunks s, s + 8, ..,
-// then the slices are added in order.
-constexpr int kSlices = 8;
-
-__global__ void __launch_bounds__(32 * kSlices)
-    linear_db_kernel(const int32_t* __restrict__ offsets, int rows, int E, int N,
-                     const float* __restrict__ part, float* __restrict__ db) {
-    __shared__ float4 s_sum[kSlices][32];
-    __shared__ int off[kMaxExperts + 1];
-    pdl_wait();
-    pdl_launch_dependents();
-    if (threadIdx.x < 32) load_group_bounds(offsets, E, rows, off);
-    __syncthreads();
-    const int e = blockIdx.y, lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const int c = (blockIdx.x * 32 + lane) * 4;
-    int first = 0;
-    for (int g = 0; g < e; ++g) first += (off[g + 1] - off[g] + kTailRows - 1) / kTailRows;
-    const int chunks = (off[e + 1] - off[e] + kTailRows - 1) / kTailRows;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < N) {
-#pragma unroll 4
-        for (int k = slice; k < chunks; k += kSlices) {
-            const float4 p =
-                *reinterpret_cast<const float4*>(part + static_cast<size_t>(first + k) * N + c);
-            s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
-        }
-    }
-    s_sum[slice][lane] = s;
-    __syncthreads();
-    if (slice != 0 || c >= N) return;
-    for (int k = 1; k < kSlices; ++k) {
-        const float4 p = s_sum[k][lane];
-        s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
-    }
-    *reinterpret_cast<float4*>(db + static_cast<size_t>(e) * N + c) = s;
+    for (int item = blockIdx.x; item < a.items; item += gridDim.x) dz_item(a, off, s_sum, s_last, item);
 }
 
 }  // namespace
@@ -194,20 +200,21 @@ cudaError_t launch_linear_dz(const LinearBwdArgs& a) {
     d.dz = static_cast<__nv_bfloat16*>(a.dz);
     d.dz_tail = a.dW ? static_cast<__nv_bfloat16*>(a.dz_tail) : nullptr;
     d.x_tail = static_cast<__nv_bfloat16*>(a.x_tail);
-    d.by_group = a.rows <= kTailRows;
-    d.sums = a.db == nullptr ? nullptr : (d.by_group ? a.db : a.db_part);
+    d.db = a.db;
+    d.part = a.db_part;
+    d.counters = a.db_counters;
     d.n_strips = (a.N + kCols - 1) / kCols;
     d.strips = d.n_strips + (a.dW ? (a.K + kCols - 1) / kCols : 0);
-    const size_t chunks = d.by_group ? static_cast<size_t>(a.E) : linear_chunks(a.rows, a.E);
+    // Blocks stay for several items, because reading the group bounds takes a block as long
+    // as one; and chunks grow while there are several items for every block.
+    const int blocks = device_sm_count() * kBlocksPerSm;
+    long long chunks;
+    for (d.chunk_rows = kTailRows;; d.chunk_rows *= 2) {
+        chunks = a.rows / d.chunk_rows + a.E;  // at most linear_chunks
+        if (d.chunk_rows >= 512 || chunks * d.strips < 6LL * blocks) break;
+    }
     d.items = static_cast<int>(chunks * d.strips);  // rows * N, rows * K < 2^40: below 2^31
-    // Blocks stay for several items: reading the group bounds takes a block as long as one.
-    const int most = device_sm_count() * kBlocksPerSm;
-    cudaError_t err = launch_k(linear_dz_kernel, d.items < most ? d.items : most, kThreads, 0,
-                               a.stream, d);
-    if (err == cudaSuccess && a.db != nullptr && !d.by_group)
-        err = launch_k(linear_db_kernel, dim3((a.N + 127) / 128, a.E), 32 * kSlices, 0, a.stream,
-                       a.offsets, a.rows, a.E, a.N, static_cast<const float*>(a.db_part), a.db);
-    return err;
+    return launch_k(linear_dz_kernel, d.items < blocks ? d.items : blocks, kThreads, 0, a.stream, d);
 }
 
 }  // namespace moe

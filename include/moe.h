@@ -309,7 +309,8 @@ typedef enum {
 /* Bytes of workspace moe_grouped_linear and moe_grouped_linear_train need for this
  * shape; never decreasing in rows.  Zero the workspace once before its first use: it
  * holds a status word (offset 0, moe_device_status) and counters that every completed
- * call leaves at zero (zero it again after MOE_DEV_FLAG_TIMEOUT).  Calls that may run at
+ * call leaves at zero (zero it again after MOE_DEV_FLAG_TIMEOUT).  One that is large
+ * enough serves calls of any shapes and both directions in turn.  Calls that may run at
  * the same time -- on two streams, or in two captured graphs -- each need their own.
  * Returns 0 for unsupported arguments. */
 size_t moe_grouped_linear_workspace_bytes(int rows, int K, int N, int E, moe_dtype dt);

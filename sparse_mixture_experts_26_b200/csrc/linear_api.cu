@@ -31,9 +31,11 @@ bool valid_act(moe_act act) { return act >= MOE_ACT_NONE && act <= MOE_ACT_SILU;
 bool valid_dt(moe_dtype dt) { return dt == MOE_F32 || dt == MOE_BF16; }
 bool optional_ok(const void* p) { return aligned16(p); }  // null is aligned
 
-// Workspace regions (1 KiB aligned): status word, counters.
+// Workspace regions (1 KiB aligned).  The status word and the counters, which are zero between
+// calls, come first and have the same place for every shape and for both directions: one
+// workspace may serve them all in turn.
 struct LinearWs {
-    size_t status, counters, partials, dz, dz_tail, x_tail, db_part, db_counters, total;
+    size_t status, counters, db_counters, partials, dz, dz_tail, x_tail, db_part, total;
 };
 LinearWs linear_ws(int rows, int K, int N, int E, moe_dtype dt, bool backward) {
     LinearWs L{};
@@ -45,13 +47,13 @@ LinearWs linear_ws(int rows, int K, int N, int E, moe_dtype dt, bool backward) {
     };
     L.status = take(256);
     L.counters = take(kLinearCounters * 4);
+    L.db_counters = take(kLinearDbCounters * 4);
     L.partials = take(dt == MOE_BF16 ? linear_partial_floats(rows) * 4 : 0);
     const size_t b = backward ? 1 : 0, tail = b * E * kTailRows;
     L.dz = take(b * rows * N * 2);
     L.dz_tail = take(tail * N * 2);
     L.x_tail = take(tail * K * 2);
     L.db_part = take(b * linear_chunks(rows, E) * N * 4);
-    L.db_counters = take(b * linear_db_counters(N, E) * 4);
     L.total = o;
     return L;
 }

@@ -206,12 +206,18 @@ cudaError_t launch_linear_dz(const LinearBwdArgs& a) {
     d.n_strips = (a.N + kCols - 1) / kCols;
     d.strips = d.n_strips + (a.dW ? (a.K + kCols - 1) / kCols : 0);
     // Blocks stay for several items, because reading the group bounds takes a block as long
-    // as one; and chunks grow while there are several items for every block.
+    // as one; and chunks grow while there are several items for every block.  Where the
+    // counters are too few, a group is one chunk: its strips (more than 256) are work enough.
     const int blocks = device_sm_count() * kBlocksPerSm;
     long long chunks;
-    for (d.chunk_rows = kTailRows;; d.chunk_rows *= 2) {
-        chunks = a.rows / d.chunk_rows + a.E;  // at most linear_chunks
-        if (d.chunk_rows >= 512 || chunks * d.strips < 6LL * blocks) break;
+    if (static_cast<long long>(a.E) * d.n_strips > kLinearDbCounters) {
+        d.chunk_rows = (a.rows + kTailRows - 1) / kTailRows * kTailRows;
+        chunks = a.E;
+    } else {
+        for (d.chunk_rows = kTailRows;; d.chunk_rows *= 2) {
+            chunks = a.rows / d.chunk_rows + a.E;  // at most linear_chunks
+            if (d.chunk_rows >= 512 || chunks * d.strips < 6LL * blocks) break;
+        }
     }
     d.items = static_cast<int>(chunks * d.strips);  // rows * N, rows * K < 2^40: below 2^31
     return launch_k(linear_dz_kernel, d.items < blocks ? d.items : blocks, kThreads, 0, a.stream, d);

@@ -341,7 +341,7 @@ struct LinearBwdArgs {
     void* dz_tail;           // bf16 [E * kTailRows, N]: each group's last, partial block of
     void* x_tail;            // bf16 [E * kTailRows, K]  rows, followed by zero rows
     float* db_part;          // [linear_chunks(rows, E), N]
-    uint32_t* db_counters;   // linear_db_counters(N, E) words, zero between calls
+    uint32_t* db_counters;   // kLinearDbCounters words, zero between calls
     uint32_t* status;
     uint32_t* counters;
     float* partials;
@@ -350,7 +350,8 @@ struct LinearBwdArgs {
 constexpr int kTailRows = 64;
 // Blocks of up to kTailRows rows of one group, at most.
 inline size_t linear_chunks(int rows, int E) { return static_cast<size_t>(rows) / kTailRows + E; }
-inline size_t linear_db_counters(int N, int E) { return static_cast<size_t>(E) * ((N + 255) / 256); }
+// One for each group and 256 features; shapes with more of them join no chunks.
+constexpr int kLinearDbCounters = 8192;
 cudaError_t launch_linear_backward(const LinearBwdArgs& a);
 // dz, the tails and db (linear_rows.cu); dW from them (grouped_linear_wgrad_sm100.cu).
 cudaError_t launch_linear_dz(const LinearBwdArgs& a);

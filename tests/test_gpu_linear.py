@@ -553,6 +553,39 @@ def test_one_workspace_serves_smaller_batches():
         check_gradients(dx, dW, db, t, None, "none", counts)
 
 
+def test_one_workspace_serves_other_shapes_and_directions_in_turn():
+    """Long groups, whose bias gradients are joined from several chunks, after calls of other
+    shapes that fill the same bytes with values."""
+    shapes = [((700, 513), 264, 1032), ((300, 0, 500, 90), 1032, 264), ((900,), 136, 2056),
+              ((5, 3), 4104, 520), ((1100, 400), 520, 72)]
+    bws = torch.zeros(max(moe.moe_grouped_linear_backward_workspace_bytes(sum(c), K, N, len(c))
+                          for c, K, N in shapes), dtype=torch.uint8, device="cuda")
+    for turn in range(2):
+        for i, (counts, K, N) in enumerate(shapes):
+            n, E = sum(counts), len(counts)
+            t = R.inputs(counts, K, N, bf, 200 + 10 * turn + i)
+            off = R.offsets_of(counts)
+            y = torch.empty(n, N, dtype=bf, device="cuda")
+            codes, scales = moe.alloc_checkpoint(n, N)
+            moe.moe_grouped_linear_train(t["x"], off, t["W"], y, codes, scales, bws,
+                                         bias=t["bias"], act="relu")
+            check_y(y, t, counts, K, "relu", n)
+            dx, dW = torch.empty_like(t["x"]), torch.empty_like(t["W"])
+            db = torch.full((E, N), 9.0, device="cuda")
+            moe.moe_grouped_linear_backward(t["dy"], t["x"], off, t["W"], bws, dx=dx, dW=dW, db=db,
+                                            codes=codes, scales=scales, act="relu")
+            check_gradients(dx, dW, db, t, R.values(codes, scales), "relu", counts)
+    assert moe.moe_device_status(bws) == 0
+
+
+def test_bias_gradient_with_more_strips_than_counters():
+    K, N, counts = 8, 65792, (70, 0, 1) + (0,) * 28 + (129,)
+    assert len(counts) * (N // 256) > 8192
+    t = R.inputs(counts, K, N, bf, 7, bias=False)
+    dx, dW, db, zhat, *_ = run_backward(t, counts, "relu")
+    check_gradients(dx, dW, db, t, zhat, "relu", counts)
+
+
 def test_nothing_is_written_outside_the_outputs():
     guard = 4096
 

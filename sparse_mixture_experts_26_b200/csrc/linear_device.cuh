@@ -22,6 +22,13 @@ __device__ __forceinline__ float ex2_approx(float v) {
     return r;
 }
 
+// The larger one, or NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Two floats in a 64-bit register: one instruction works on both.
 using F2 = unsigned long long;
 __device__ __forceinline__ F2 f2(float a, float b) {
@@ -79,25 +86,28 @@ __device__ __forceinline__ void sigmoids(float z0, float z1, float& s0, float& s
     s1 = r * d0;
 }
 
-// v = act(v).  A NaN stays one; an infinity gives an infinity or NaN.
-//   GELU: z Phi(z) = max(z, 0) - |z| Phi(-|z|)
+// v = act(v), also far out: a NaN stays one (and leaves its neighbour alone), infinities give
+// the limits.
+//   GELU: z Phi(z) = max(z, 0) - |z| Phi(-|z|), |z| at most 24, where Phi is zero
+//   SiLU: z at least -43, as in sigmoids()
 __device__ __forceinline__ void act_value8(int act, float (&v)[8]) {
     if (act == MOE_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
             F2 e;
             float t0, t1;
-            f2_get(normal_tails(fminf(fabsf(v[i]), 24.f), fminf(fabsf(v[i + 1]), 24.f), e), t0, t1);
-            v[i] = fmaf(-fabsf(v[i]), t0, fmaxf(v[i], 0.f));
-            v[i + 1] = fmaf(-fabsf(v[i + 1]), t1, fmaxf(v[i + 1], 0.f));
+            const float x0 = fminf(fabsf(v[i]), 24.f), x1 = fminf(fabsf(v[i + 1]), 24.f);
+            f2_get(normal_tails(x0, x1, e), t0, t1);
+            v[i] = fmaf(-x0, t0, max_nan(v[i], 0.f));
+            v[i + 1] = fmaf(-x1, t1, max_nan(v[i + 1], 0.f));
         }
     } else if (act == MOE_ACT_SILU) {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
             float s0, s1;
             sigmoids(v[i], v[i + 1], s0, s1);
-            v[i] *= s0;
-            v[i + 1] *= s1;
+            v[i] = max_nan(v[i], -43.f) * s0;
+            v[i + 1] = max_nan(v[i + 1], -43.f) * s1;
         }
     } else if (act == MOE_ACT_RELU) {
 #pragma unroll
@@ -128,7 +138,8 @@ __device__ __forceinline__ void act_slope8(int act, const float (&z)[8], float (
             float s[2];
             sigmoids(z[i], z[i + 1], s[0], s[1]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) g[i + k] *= s[k] * fmaf(z[i + k], 1.0f - s[k], 1.0f);
+            for (int k = 0; k < 2; ++k)
+                g[i + k] *= s[k] * fmaf(max_nan(z[i + k], -43.f), 1.0f - s[k], 1.0f);
         }
     } else if (act == MOE_ACT_RELU) {
 #pragma unroll
@@ -137,7 +148,7 @@ __device__ __forceinline__ void act_slope8(int act, const float (&z)[8], float (
 }
 
 // a / b and the remainder, 0 <= a < 2^31, b > 0: the quotient of the rounded floats is off by
-// a few at most.  (A tile's decode stands between two tiles; integer divisions there cost
+// one, or by 2^-21 of a large quotient.  (A tile's decode stands between two tiles; integer divisions there cost
 // the tensor cores about 1000 cycles a tile.)
 __device__ __forceinline__ int divide(int a, int b, int& remainder) {
     int q = __float2int_rd(static_cast<float>(a) * rcp_approx(static_cast<float>(b)));
@@ -152,11 +163,6 @@ constexpr int kCkptBlock = MOE_CHECKPOINT_BLOCK;
 inline __host__ __device__ int ckpt_blocks(int n) { return (n + kCkptBlock - 1) / kCkptBlock; }
 
 // Largest magnitude of eight values; a NaN is larger than all, so that it reaches the scale.
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
 __device__ __forceinline__ float ckpt_amax8(const float (&v)[8]) {
     float m = fabsf(v[0]);
 #pragma unroll

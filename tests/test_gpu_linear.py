@@ -94,6 +94,60 @@ def test_residual_may_be_the_output():
         assert torch.equal(y, inout)
 
 
+FAR = [0.0, 2.0 ** -100, 1.0, 5.9375, 20.0, 42.5, 50.0, 100.0, 2.0 ** 13, 2.0 ** 40, 2.0 ** 80,
+       2.0 ** 127]
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+@pytest.mark.parametrize("name", R.ACTS)
+def test_activations_of_far_out_values(name, dtype):
+    """z is the bias: huge values of either sign, and infinities and NaN, whose neighbours keep
+    their own results."""
+    z = torch.tensor([s * v for v in FAR for s in (1, -1)], dtype=torch.float64, device="cuda")
+    rows, K, N = 5, 16, 2 * len(FAR) + 8
+    special = {1: float("nan"), 4: float("inf"), 11: -float("inf"), 18: float("nan")}
+    for with_special in (False, True):
+        b = torch.cat([z, z[:8]])
+        if with_special:
+            for i, v in special.items():
+                b[i] = v
+        b = b.to(dtype)
+        x = torch.zeros(rows, K, dtype=dtype, device="cuda")
+        W = torch.ones(1, N, K, dtype=dtype, device="cuda")
+        y = moe.grouped_linear(x, None, W, b[None], act=name).double()
+        zz = b.double()
+        ref = R.act(zz, name)
+        if name != "none":  # the limit, where the formula is 0 times infinity
+            ref = torch.where(zz == -float("inf"), torch.zeros_like(ref), ref)
+        u = R.U_BF16 if dtype == bf else 2.0 ** -23
+        nan = zz.isnan()
+        assert bool((y.isnan() == nan).all())
+        inf = ref.isinf()
+        assert bool((y[:, inf] == ref[inf]).all())
+        ok = ~nan & ~inf
+        # the activation's own error goes with |z| where z is of order one and vanishes far out
+        tol = u * ref.abs() + (0 if name in ("none", "relu") else
+                               R.ACT_ERR * (1 + zz.abs().clamp(max=10)) * (zz.abs() < 40) + 1e-15)
+        assert bool(((y - ref).abs()[:, ok] <= tol[ok]).all())
+
+
+@pytest.mark.parametrize("name", ["relu", "gelu", "silu"])
+@pytest.mark.parametrize("scale", [2.0 ** 8, 2.0 ** 60, 2.0 ** 120])
+def test_slopes_of_far_out_values(name, scale):
+    """Values of at least 128: the slope is one or zero by the sign."""
+    rows, N = 70, 40
+    g = torch.Generator(device="cuda").manual_seed(4)
+    codes = torch.randint(-128, 128, (rows, N), generator=g, device="cuda", dtype=torch.int8)
+    scales = torch.full((rows, 2), scale, device="cuda")
+    dy = torch.randint(-8, 9, (rows, N), generator=g, device="cuda").to(bf)
+    x, W = torch.zeros(rows, 8, dtype=bf, device="cuda"), torch.zeros(1, N, 8, dtype=bf,
+                                                                      device="cuda")
+    db = torch.empty(1, N, device="cuda")
+    ws = moe.alloc_grouped_linear_backward_workspace(rows, 8, N, 1)
+    moe.moe_grouped_linear_backward(dy, x, None, W, ws, db=db, codes=codes, scales=scales, act=name)
+    assert bool(((db[0].double() - (dy.double() * (codes >= 0)).sum(0)).abs() <= 1e-12).all())
+
+
 # ------------------------------------------------------------------------- checkpoint
 @pytest.mark.parametrize("dtype", [bf, f32])
 @pytest.mark.parametrize("rows,N", [(1, 8), (1, 32), (3, 40), (65, 72), (7, 7168), (1000, 264)])

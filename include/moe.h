@@ -297,6 +297,8 @@ moe_status moe_layer_backward_events(const void *x, const void *Wg, const void *
  * all rows.  Groups may be empty.  Rows behind the last group (offsets[E] .. rows-1) are
  * neither computed nor written, and what x, dy, residual and the checkpoint hold there
  * -- infinities and NaN included -- reaches no result.
+ * Buffers are contiguous, 16-byte aligned (offsets and the workspace too) and overlap
+ * only where stated.
  * Shapes: K and N multiples of 8, 1 <= E <= 32, any rows >= 0 (rows == 0 queues
  * nothing, except that moe_grouped_linear_backward writes zero dW and db). */
 typedef enum {
@@ -340,7 +342,8 @@ moe_status moe_grouped_linear(const void *x, const int32_t *offsets, const void 
 
 /* moe_grouped_linear for training: the same y, and the pre-activations z kept as an
  * 8-bit checkpoint (codes, scales) for moe_grouped_linear_backward: 1.125 bytes a
- * value.  z is taken from the fp32 accumulator.  dt must be MOE_BF16
+ * value.  z is taken from the fp32 accumulator; where z / s is less than about 2^-15 above a
+ * whole number, the code may be the one below.  dt must be MOE_BF16
  * (MOE_ERR_UNSUPPORTED otherwise). */
 moe_status moe_grouped_linear_train(const void *x, const int32_t *offsets, const void *W,
                                     const void *bias, const void *residual, int rows, int K,

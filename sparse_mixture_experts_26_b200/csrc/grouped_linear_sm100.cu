@@ -18,19 +18,22 @@
 // are K-major; the transposed product reads the same weights MN-major (64 x 64 boxes).
 //
 // Epilogue: TMEM lanes are features and columns tokens, so a warp turns its 32 features x
-// eight tokens at a time in shared memory of its own (neither side meets a bank twice) and comes back with eight consecutive features of one token per thread:
-// bias, residual, activation and the output are 16-byte accesses, 64 bytes of a row
-// together, and a checkpoint block of 32 features is four neighbouring lanes (two shuffles
-// for its largest magnitude).  Sixteen warps, because the rounds are chains of latencies.
+// eight tokens at a time in shared memory of its own (neither side meets a bank twice) and
+// comes back with eight consecutive features of one token per thread: bias, residual,
+// activation and the output are 16-byte accesses, 64 bytes of a row together, and a
+// checkpoint block of 32 features is four neighbouring lanes (two shuffles for its largest
+// magnitude).  Sixteen warps, because the rounds are chains of latencies.
 //
 // Split reduction (single SMs): tiles are dealt out round by round.  Where the last round
 // would leave SMs idle, its tiles are cut along the reduction instead (equal shares of all
 // remaining 64-steps, at most two tiles each): every share's fp32 tile goes to the
 // workspace, and the CTA that finishes a tile last adds the shares in the order of the
 // reduction, whoever it is, so the result does not depend on the timing; nobody waits for
-// anybody.  Pairs do not
-// share: they run at the power limit, where an idle SM lets the others clock higher (4096 x
-// 14336 x 4096: 1286 TFLOP/s unshared, 1232 shared).
+// anybody.  Pairs do not share: they run at the power limit, where an idle SM lets the others
+// clock higher (4096 x 14336 x 4096: 1286 TFLOP/s unshared, 1232 shared).
+//
+// Measured: 4096^3 1400 TFLOP/s, 8192 x 4096 x 14336 1263 to 1372 (cuBLAS 1493 and 1310);
+// 8 experts, 32 rows, 14336 -> 4096 in 134 to 144 us, 98 to 106 % of a copy's bandwidth.
 //
 // Every wait is bounded (sm100_ptx.cuh).
 #include <cuda.h>

@@ -29,10 +29,6 @@ namespace moe {
 // Defined in grouped_gemm_sm100.cu.
 bool encode_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                     uint32_t box_rows);
-bool encode_bf16_3d(CUtensorMap* map, const void* base, uint64_t batches, uint64_t rows,
-                    uint64_t cols, uint32_t box_rows);
-bool encode_f32_3d(CUtensorMap* map, const void* base, uint64_t batches, uint64_t rows,
-                   uint64_t cols, uint32_t box_cols, uint32_t box_rows);
 
 namespace {
 

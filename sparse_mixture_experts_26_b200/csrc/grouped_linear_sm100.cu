@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* staging = reinterpret_cast<float*>(smem + kRingBytes);
     Book& bk = *reinterpret_cast<Book*>(smem + kRingBytes + kStagingBytes);
     volatile int* abort_flag = &bk.abort_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
     const bool leader = rank == 0;
     const int ftiles = (args.F + kTileF - 1) / kTileF;
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        if (lane == 0) {
+        if (elect_one()) {
             int stage = 0;
             uint32_t phase = 0, pending = 0, pending_phase = 0;
             bool ok = true, issued = false;
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (leader)
-        if (lane == 0 && leader) {
+        if (leader && elect_one()) {
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true, issued = false;

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
     uint8_t* staging = smem + STAGES * S::kStageBytes;
     auto& bk = *reinterpret_cast<Book<STAGES>*>(staging + S::kStaging);
     volatile int* abort_flag = &bk.abort_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
     const bool leader = rank == 0;
 
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
     int e, m0, n0, row0, n;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             int stage = 0;
             uint32_t phase = 0, pending = 0, pending_phase = 0;
             bool ok = true, issued = false;
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader && elect_one()) {
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true, issued = false;

@@ -73,19 +73,43 @@ constexpr int kVoteBarrier = 1;
 constexpr int kJoinBarrier = 2;
 constexpr uint16_t kBothCtas = 0x3;
 constexpr int kMinShare = 4;           // 64-steps of a share, at least
+constexpr int kPrefetchSteps = 20;     // 64-steps of a tile up to which its residual is prefetched
 
-// What a CTA's work takes, in clocks; rough, to choose among layouts.  A stage of 128
-// features x `width` tokens: the tensor core's time (two clocks a token; on a pair both
-// halves) or the bytes from L2, 36 a clock and SM for single SMs and 55 for pairs, as
-// measured.  Joining shares: rounds of 32 tokens and four shares, each a memory latency.
-__host__ __device__ inline float stage_clocks(int width, bool pair) {
-    const float tensor = 2.f * width;
-    const float bytes = 16384.f + 128.f * (pair ? width / 2 : width);
-    const float load = bytes / (pair ? 55.f : 36.f);
-    return tensor > load ? tensor : load;
+// What a CTA's work takes, in clocks; fitted to measurements, to choose among layouts.  A
+// stage of 128 features x `width` tokens: the tensor core's time, two clocks a token (on a pair
+// both halves), or what issuing it or loading its 128-byte rows takes.  Measured with rows on
+// 128-byte boundaries:
+//   width            32   64   96  128  160  192  224  256
+//   pairs, clocks   270  280  302  333  369  399  461  517
+//   single SMs      295  309  339  390  453  484  596  625
+// Rows that lie across two lines take longer, most of all across 32-byte sectors (3 groups, 300
+// rows, K -> 5000, us on pairs and on single SMs: K = 4992 31 and 29, 5024 31 and 38, 5008 32
+// and 39, 5000 33 and 45).
+struct RowClocks {
+    float w, x;  // a row of weights, of tokens
+};
+inline float row_clocks(int length) {
+    return length % 64 == 0 ? 1.6f : (length % 16 == 0 ? 2.4f : 4.1f);
 }
-// Pairs: a cluster's launch and its two synchronisations, without programmatic launch.
-constexpr float kJoinClocks = 2200.f, kShareClocks = 3000.f, kPairClocks = 3000.f;
+__host__ __device__ inline float stage_clocks(int width, bool pair, RowClocks row) {
+    const float w = static_cast<float>(width);
+    const float tensor = 2.02f * w;
+    const float issue = pair ? 230.f + 0.8f * w : 245.f + 1.15f * w;
+    const float load = kF * row.w + (pair ? 0.5f : 1.f) * w * row.x;
+    return fmaxf(fmaxf(tensor, issue), load);
+}
+// A tile's epilogue with its turn of the accumulators; 256 and 128 tokens measured: plain 6700
+// and 4300, with a GELU 9600 and 5900, with the checkpoint too 12000 and 7000; single SMs a
+// tenth more.
+inline float epilogue_clocks(const LinearArgs& a, int width, bool pair) {
+    const float token = 19.f + (a.act >= MOE_ACT_GELU ? 10.f : 0.f) +
+                        (a.codes != nullptr ? 10.f : 0.f) + (a.residual != nullptr ? 12.f : 0.f);
+    return (pair ? 1.f : 1.1f) * (1900.f + token * static_cast<float>(width));
+}
+// Pairs: a cluster's launch and its two synchronisations, without programmatic launch (4
+// groups, 1900 rows, 1472 -> 1504: 16.5 us on pairs, 13.5 on single SMs).  Shares: writing one,
+// and the joins below.
+constexpr float kJoinClocks = 2200.f, kShareClocks = 3000.f, kPairClocks = 6500.f;
 
 // How many CTAs (0: none) share the reduction of the last `rem` tiles, and the clocks.  No
 // integer division: every thread goes through this before its first piece of work.
@@ -93,8 +117,8 @@ constexpr int kMostSteps = 1 << 15;  // of a shared reduction: 160 x 160 of them
 struct Sharing {
     int ctas;
     float clocks;
-    __host__ __device__ Sharing(int rem, int num_kb, int width, int G) {
-        const float stage = stage_clocks(width, false), whole = num_kb * stage;
+    __host__ __device__ Sharing(int rem, int num_kb, int width, int G, RowClocks row) {
+        const float stage = stage_clocks(width, false, row), whole = num_kb * stage;
         ctas = 0;
         clocks = whole;
         if (rem == 0 || num_kb < 2 * kMinShare || num_kb >= kMostSteps) return;
@@ -105,13 +129,22 @@ struct Sharing {
         if (most > rem * num_kb / kMinShare) most = rem * num_kb / kMinShare;
         if (most > G) most = G;
         if (most <= rem) return;
-        const float each = static_cast<float>(most) / static_cast<float>(rem);  // shares a tile
-        const float shared = (num_kb / each + 1.f) * stage +
-                             static_cast<float>(static_cast<int>(each) / 4 + 1) * join +
-                             kShareClocks;
+        // .. all of them, or a whole number a tile, which none then crosses
+        const float each = static_cast<float>(most) / static_cast<float>(rem);
+        const float even = floorf(each);
+        const float crossing = cost(each, ceilf(each) + 1.f, num_kb, stage, join) + join +
+                               kShareClocks;  // its two pieces come after one another
+        const float aligned = even < 2.f ? crossing : cost(even, even, num_kb, stage, join);
+        const bool align = aligned <= crossing && even >= 2.f;
+        const float shared = align ? aligned : crossing;
         if (shared >= whole) return;
-        ctas = most;
+        ctas = align ? static_cast<int>(even) * rem : most;
         clocks = shared;
+    }
+    // `each` shares a tile on average, `most` at most: the join adds four at a time
+    __host__ __device__ static float cost(float each, float most, int num_kb, float stage,
+                                          float join) {
+        return (num_kb / each + 1.f) * stage + ceilf(most * 0.25f) * join + kShareClocks;
     }
 };
 
@@ -133,6 +166,7 @@ struct Args {
     uint32_t* counters;
     float* partials;
     int slot_tokens;
+    RowClocks row;
     uint32_t* status;
 };
 
@@ -202,12 +236,13 @@ struct Plan {
     int G, c, num_kb, rounds, rem, share_ctas;
     int pieces;             // of this CTA's share: 0, 1 or 2
     int first, from, to;    // the share: 64-steps from .. to, counted from its first tile
-    __device__ __forceinline__ Plan(int G_, int c_, int total, int num_kb_, int widest, bool may_share)
+    __device__ __forceinline__ Plan(int G_, int c_, int total, int num_kb_, int widest, bool may_share,
+                                    RowClocks row)
         : G(G_), c(c_), num_kb(num_kb_) {
         rounds = divide(total, G, rem);
         share_ctas = pieces = first = from = to = 0;
         if (rem > 0 && may_share) {
-            share_ctas = Sharing(rem, num_kb, widest, G).ctas;
+            share_ctas = Sharing(rem, num_kb, widest, G, row).ctas;
             if (c < share_ctas) {
                 const int u0 = bound(c), u1 = bound(c + 1);
                 first = divide(u0, num_kb, from);
@@ -335,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem_base = bk.tmem_base;
     const int stages = bk.stages, stage_bytes = bk.stage_bytes;
     const Plan plan(gridDim.x / kCtas, blockIdx.x / kCtas, bk.tile_start[args.E], num_kb,
-                    bk.widest, !PAIR);
+                    bk.widest, !PAIR, args.row);
     Pieces<kStep> cur;
     auto next_piece = [&]() { return cur.next(plan, bk, args, ftiles, kTileF); };
 
@@ -519,6 +554,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             float bias[8] = {};
             if (args.bias != nullptr && have_f)
                 load8(args.bias + static_cast<size_t>(t.e) * args.F + f, bias);
+            // Where the epilogue is the bound, the residual is fetched to L2 ahead of it: 9472 x
+            // K -> 8192 with K = 512: 134 -> 101 us, 1024: 138 -> 109, 1280: 142 -> 122; longer
+            // reductions leave it time, and there the burst only disturbs (2048: 161 -> 168).
+            // A CTA's first tile gains nothing either (600 x 1024 -> 7168: 17.8 -> 19.0).
+            if (args.residual != nullptr && have_f && num_kb <= kPrefetchSteps && i > 0) {
+                const __nv_bfloat16* p =
+                    args.residual + static_cast<size_t>(t.row0 + group * kRound + my_tok) * args.F + f;
+                for (int tok = group * kRound + my_tok; tok < t.n; tok += kEpiGroups * kRound) {
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+                    p += static_cast<size_t>(kEpiGroups * kRound) * args.F;
+                }
+            }
             // A warp that gives up leaves alone; only shares, which come before all whole
             // tiles, have barriers among the warps, and there they leave together.
             bool ok = __all_sync(0xffffffffu, mbar_wait_asleep(&bk.tmem_full[acc], acc_phase,
@@ -532,7 +579,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the eight sums of token `tok` -> checkpoint, activation, residual, output; `at`:
             // where that token's row has feature f
             const size_t origin = static_cast<size_t>(t.row0) * args.F + f;
-            auto finish = [&](int tok, size_t at, float (&v)[8]) {
+            auto residual = [&](int tok, size_t at) {
+                return args.residual != nullptr && have_f && tok < t.n
+                           ? *reinterpret_cast<const uint4*>(args.residual + at)
+                           : make_uint4(0u, 0u, 0u, 0u);
+            };
+            auto finish = [&](int tok, size_t at, float (&v)[8], uint4 res) {
                 const bool valid = have_f && tok < t.n;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] += bias[k];
@@ -548,10 +600,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!valid) return;
                 act_value8(args.act, v);
                 if (args.residual != nullptr) {
-                    float r[8];
-                    load8(args.residual + at, r);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] += r[k];
+                    v[0] += bf16_lo(res.x), v[1] += bf16_hi(res.x);
+                    v[2] += bf16_lo(res.y), v[3] += bf16_hi(res.y);
+                    v[4] += bf16_lo(res.z), v[5] += bf16_hi(res.z);
+                    v[6] += bf16_lo(res.w), v[7] += bf16_hi(res.w);
                 }
                 if (args.out_f32)
                     store8(static_cast<float*>(args.out) + at, v);
@@ -561,11 +613,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t F = static_cast<size_t>(args.F);
 
             if (whole) {
-                // round by round of 8 tokens; the next one's accumulator columns are on their
-                // way while this one is finished
+                // round by round of 8 tokens; the next one's accumulator columns and residual
+                // are on their way while this one is finished (the residual's latency alone took
+                // longer than the rest: 9472 x 512 -> 8192, 154 us with it and 75 without)
+                const size_t step = kEpiGroups * kRound * F;
                 size_t at = origin + (group * kRound + my_tok) * F;
                 uint32_t r[kRound];
                 int c0 = group * kRound;
+                uint4 next = residual(c0 + my_tok, at);
                 if (c0 < t.nt)
                     tmem_ld_8cols(tbase + c0, r);
                 else
@@ -578,11 +633,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < kRound; ++k) my_staging[k * kPitch + lane] = bits_f32(r[k]);
                     if (c1 < t.nt) tmem_ld_8cols(tbase + c1, r);
+                    const uint4 res = next;
+                    next = residual(c1 + my_tok, at + step);
                     __syncwarp();
                     float v[8];
                     load8(get, v);
-                    finish(c0 + my_tok, at, v);
-                    at += kEpiGroups * kRound * F;
+                    finish(c0 + my_tok, at, v, res);
+                    at += step;
                 }
             } else if constexpr (!PAIR) {
                 // a share: the fp32 tile to the workspace as [token][feature]
@@ -629,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
                             v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
                         }
-                        finish(tok, origin + tok * F, v);
+                        finish(tok, origin + tok * F, v, residual(tok, origin + tok * F));
                     }
                 }
             }
@@ -650,7 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-constexpr int kMinWidth = 32;  // narrowest tile limit
+constexpr int kMinWidth = 32;      // narrowest tile limit
+constexpr int kPairsAtFloor = 64;  // rows of a group
 
 int usable_sms() {
     const int sms = device_sm_count();
@@ -664,7 +722,7 @@ long long most_tiles(const LinearArgs& a, int F, int width, int features) {
 }
 
 template <bool PAIR, bool TRANSPOSED>
-cudaError_t launch_engine(const LinearArgs& a, int F, int C, int width) {
+cudaError_t launch_engine(const LinearArgs& a, int F, int C, int width, RowClocks row) {
     constexpr int kCtas = PAIR ? 2 : 1;
     auto kern = linear_sm100_kernel<PAIR, TRANSPOSED>;
     static PerDeviceOnce once;
@@ -691,6 +749,7 @@ cudaError_t launch_engine(const LinearArgs& a, int F, int C, int width) {
     g.counters = a.counters;
     g.partials = a.partials;
     g.slot_tokens = linear_slot_tokens(a.rows);
+    g.row = row;
     g.status = a.status;
     CUtensorMap w;
     TokenMaps x;
@@ -726,16 +785,20 @@ struct Layout {
 };
 
 // The layout with the least clocks for groups of the average size; the weights' bytes from
-// HBM (23 a clock and SM) are a floor for all, and of layouts at the floor the first wins:
-// single SMs, wide tiles.  Measured (us; pairs, then single SMs with tiles of up to 256, 128,
+// HBM (23 a clock and SM) are a floor for all, and of layouts at the floor the first wins: wide
+// tiles on single SMs, or on pairs from 64 rows a group on (uniform groups take the same time
+// there, a group that is larger than the average less: 8 skewed groups, 600 rows, 7168 -> 2048
+// 48 us on pairs and 54 on single SMs).  Measured (us; pairs, then single SMs with tiles of up to 256, 128,
 // 64 and 32 tokens):
-//   8 groups, 256 rows, K 4096, N 14336       158  149  149  149  186
-//   8 groups, 2048 rows, K 4096, N 14336      227  252  291  448  856
-//   1 group, 256 rows, K 4096, N 14336         33   35   40   62  109
-//   2 groups, 3968 rows, K 11512, N 136        76   57   51   60   86
-//   1 group, 1496 rows, K 5144, N 192          39   49   26   22   26
-//   1 group, 100 rows, K 8192, N 1024          39   36   36   20   20
-Layout choose_layout(const LinearArgs& a, int F, int C) {
+//   8 groups, 256 rows, K 4096, N 14336       144  137  138  138  153
+//   8 groups, 2048 rows, K 4096, N 14336      204  233  243  296  432
+//   1 group, 256 rows, K 4096, N 14336         31   34   40   42   61
+//   2 groups, 3968 rows, K 11512, N 136        78   48   50   58   84
+//   1 group, 1496 rows, K 5144, N 192          40   31   23   18   25
+//   1 group, 100 rows, K 8192, N 1024          27   17   17   15   13
+//   1 group, 512 rows, K 4096, N 4096          28   27   19   25   37
+//   1 group, 8192 rows, K 512, N 7168          60   66   75   99  181
+Layout choose_layout(const LinearArgs& a, int F, int C, RowClocks row) {
     const int sms = usable_sms();
     const int groups = a.rows < a.E ? a.rows : a.E;
     const int n = (a.rows + groups - 1) / groups;
@@ -752,21 +815,31 @@ Layout choose_layout(const LinearArgs& a, int F, int C) {
         if (clocks < floor) clocks = floor;
         if (least == 0.f || clocks < least) best = {pair, width}, least = clocks;
     };
+    // `rounds` whole tiles after one another, the epilogues beside the next one's products,
+    // the last one's behind them
+    auto whole = [&](long long rounds, int wide, bool pair) {
+        const float products = num_kb * stage_clocks(wide, pair, row);
+        const float epilogue = epilogue_clocks(a, wide, pair);
+        return rounds == 0 ? 0.f
+                           : static_cast<float>(rounds) * fmaxf(products, epilogue) + epilogue;
+    };
+    auto offer_pairs = [&]() {
+        if (!pair_gemm_enabled()) return;
+        int wide;
+        const long long all = tiles(kTokens, 2 * kF, 32, wide), pairs = sms / 2;
+        offer(true, kTokens, whole((all + pairs - 1) / pairs, wide, true) + kPairClocks);
+    };
+    if (n >= kPairsAtFloor) offer_pairs();
     for (int width = kTokens; width >= kMinWidth; width /= 2) {
         int wide;
         const long long all = tiles(width, kF, 16, wide);
         const int rem = static_cast<int>(all % sms);
-        float clocks = static_cast<float>(all / sms) * num_kb * stage_clocks(wide, false);
-        if (rem > 0) clocks += Sharing(rem, num_kb, wide, sms).clocks;
-        offer(false, width, clocks);
+        const Sharing shared(rem, num_kb, wide, sms, row);
+        offer(false, width,
+              shared.ctas > 0 ? whole(all / sms, wide, false) + shared.clocks
+                              : whole((all + sms - 1) / sms, wide, false));
     }
-    if (pair_gemm_enabled()) {
-        int wide;
-        const long long all = tiles(kTokens, 2 * kF, 32, wide), pairs = sms / 2;
-        offer(true, kTokens,
-              static_cast<float>((all + pairs - 1) / pairs) * num_kb * stage_clocks(wide, true) +
-                  kPairClocks);
-    }
+    if (n < kPairsAtFloor) offer_pairs();
     return best;
 }
 
@@ -774,15 +847,16 @@ Layout choose_layout(const LinearArgs& a, int F, int C) {
 
 cudaError_t launch_linear_bf16(const LinearArgs& a, bool transposed) {
     const int F = a.N, C = a.K;
-    const Layout l = choose_layout(a, F, C);
+    const RowClocks row = {row_clocks(transposed ? F : C), row_clocks(C)};
+    const Layout l = choose_layout(a, F, C, row);
     if (l.pair) {
-        const cudaError_t err = transposed ? launch_engine<true, true>(a, F, C, l.width)
-                                           : launch_engine<true, false>(a, F, C, l.width);
+        const cudaError_t err = transposed ? launch_engine<true, true>(a, F, C, l.width, row)
+                                           : launch_engine<true, false>(a, F, C, l.width, row);
         if (err == cudaSuccess || err == cudaErrorInvalidValue) return err;
         cudaGetLastError();  // no room for a pair of CTAs: single SMs
     }
-    return transposed ? launch_engine<false, true>(a, F, C, l.width)
-                      : launch_engine<false, false>(a, F, C, l.width);
+    return transposed ? launch_engine<false, true>(a, F, C, l.width, row)
+                      : launch_engine<false, false>(a, F, C, l.width, row);
 }
 
 }  // namespace moe

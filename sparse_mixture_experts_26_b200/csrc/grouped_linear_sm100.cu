@@ -99,11 +99,12 @@ __host__ __device__ inline float stage_clocks(int width, bool pair, RowClocks ro
     return fmaxf(fmaxf(tensor, issue), load);
 }
 // A tile's epilogue with its turn of the accumulators; 256 and 128 tokens measured: plain 6700
-// and 4300, with a GELU 9600 and 5900, with the checkpoint too 12000 and 7000; single SMs a
-// tenth more.
+// and 4300, with a GELU 9600 and 5900; single SMs a tenth more.  (With the checkpoint 12000 and
+// 7000, which does not count here: training and inference take the same layout and so give the
+// same y to the bit.)
 inline float epilogue_clocks(const LinearArgs& a, int width, bool pair) {
     const float token = 19.f + (a.act >= MOE_ACT_GELU ? 10.f : 0.f) +
-                        (a.codes != nullptr ? 10.f : 0.f) + (a.residual != nullptr ? 12.f : 0.f);
+                        (a.residual != nullptr ? 12.f : 0.f);
     return (pair ? 1.f : 1.1f) * (1900.f + token * static_cast<float>(width));
 }
 // Pairs: a cluster's launch and its two synchronisations, without programmatic launch (4

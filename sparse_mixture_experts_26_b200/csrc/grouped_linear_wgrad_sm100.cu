@@ -3,7 +3,7 @@
 //   dW[e, n, k] = sum over the rows r of group e of dz[r, n] x[r, k]
 // Both operands are rows as they lie in memory (n and k contiguous), read as MN-major
 // 64 x 64 boxes; nothing is transposed.  A tile is 128 features n (256 on a pair of SMs,
-// 128 from each) x 256 inputs k, the reduction runs over the group's rows in blocks of 64.
+// 128 from each) x up to 256 inputs k, the reduction runs over the group's rows in blocks of 64.
 //
 // A group starts and ends anywhere.  Its whole blocks come straight from dz and x; the rest
 // comes from the tail buffers (linear_rows.cu), where the group's last rows are followed
@@ -33,7 +33,8 @@ bool encode_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
 namespace {
 
 constexpr int kM = 128;              // features per CTA (TMEM lanes)
-constexpr int kN = 256;              // inputs per tile
+constexpr int kN = 256;              // inputs per tile, at most
+constexpr int kMaxStages = 8;
 constexpr int kBlock = kTailRows;    // rows of a whole block; a stage holds one or two
 constexpr int kChunk = 32 * 128;     // staged output: 32 rows x 128 bytes
 constexpr uint16_t kBothCtas = 0x3;
@@ -43,15 +44,15 @@ struct Args {
     int E, rows;
     int M;         // features (dz columns)
     int N;         // inputs (x columns)
+    int width;     // inputs of a tile: 64, 128 or 256
     int m_tiles, n_tiles;
     void* out;     // [E, M, N]
     uint32_t* status;
 };
 
-template <int STAGES>
 struct Book {
-    uint64_t full[STAGES];
-    uint64_t empty[STAGES];
+    uint64_t full[kMaxStages];
+    uint64_t empty[kMaxStages];
     uint64_t tmem_full[2];
     uint64_t tmem_empty[2];
     uint64_t drain;
@@ -63,6 +64,7 @@ struct Book {
 // GROUPS: epilogue groups of four warps, one for each quarter of the lanes; the groups take
 // the output's 128-byte columns in turn.
 // ROWS: the reduction per stage (64 or 128): with 128, half as many loads of twice the size.
+// STAGES: of tiles with 256 inputs; narrower ones have more of them.
 template <bool PAIR, int ROWS, int STAGES, int GROUPS>
 struct Shape {
     static constexpr int kBox = 128 * ROWS;  // 64 columns of a stage's rows
@@ -74,7 +76,7 @@ struct Shape {
     static constexpr int kStaging = kEpiWarps * kChunk;
     static constexpr int kSmem = STAGES * kStageBytes + kStaging + 1024 /*book*/ + 1024 /*align*/;
     static_assert(kSmem <= 232448, "shared memory");
-    static_assert(sizeof(Book<STAGES>) <= 1024, "bookkeeping reserve");
+    static_assert(sizeof(Book) <= 1024, "bookkeeping reserve");
 };
 
 template <bool PAIR, bool F32, int ROWS, int STAGES, int GROUPS>
@@ -89,20 +91,22 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
                         const __grid_constant__ CUtensorMap tmXs, const Args args) {
     using S = Shape<PAIR, ROWS, STAGES, GROUPS>;
     constexpr int kCtas = PAIR ? 2 : 1;
-    constexpr uint32_t kIdesc = idesc_bf16_f32_major(kM * kCtas, kN, true, true);
     constexpr uint32_t kTmemCols = 2 * kN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* staging = smem + STAGES * S::kStageBytes;
-    auto& bk = *reinterpret_cast<Book<STAGES>*>(staging + S::kStaging);
+    Book& bk = *reinterpret_cast<Book*>(staging + S::kStaging);
+    const int boxes = args.width / (64 * kCtas);  // of x, in a stage of this CTA
+    const int stage_bytes = S::kABytes + boxes * S::kBox;
+    const int stages = min(STAGES * S::kStageBytes / stage_bytes, kMaxStages);
     volatile int* abort_flag = &bk.abort_flag;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
     const bool leader = rank == 0;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(&bk.full[s], 1);
             mbar_init(&bk.empty[s], 1);
         }
@@ -149,9 +153,14 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
         int local, nt;
         e = divide(tile, per_e, local);
         m0 = divide(local, args.n_tiles, nt) * (kM * kCtas);
-        n0 = nt * kN;
+        n0 = nt * args.width;
         row0 = bk.off[e];
         n = bk.off[e + 1] - row0;
+    };
+    // inputs of the tile at n0 that are multiplied: whole steps of 16 on each CTA
+    auto width_of = [&](int n0) {
+        const int left = (args.N - n0 + 16 * kCtas - 1) / (16 * kCtas) * (16 * kCtas);
+        return left < args.width ? left : args.width;
     };
     int e, m0, n0, row0, n;
 
@@ -163,14 +172,15 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
             for (int tile = first; ok && tile < total; tile += step) {
                 tile_of(tile, e, m0, n0, row0, n);
                 const int mc = m0 + rank * kM;
-                const int nc = n0 + rank * (S::kBBoxes * 64);
+                const int half = width_of(n0) / kCtas;
+                const int nc = n0 + rank * half, nb = (half + 63) / 64;
                 for (int r = 0; r < n; r += ROWS) {
                     if (!mbar_wait_asleep(&bk.empty[stage], phase ^ 1u, abort_flag,
                                            args.status)) {
                         ok = false;
                         break;
                     }
-                    uint8_t* z = smem + stage * S::kStageBytes;
+                    uint8_t* z = smem + stage * stage_bytes;
                     uint8_t* x = z + S::kABytes;
                     const int left = n - r < ROWS ? n - r : ROWS;
                     auto load = [&](const CUtensorMap* map, uint8_t* dst, int c, int row) {
@@ -187,7 +197,7 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
                             load(mz, z + b * S::kBox + at * 128, mc + 64 * b, row);
 #pragma unroll
                         for (int b = 0; b < S::kBBoxes; ++b)
-                            load(mx, x + b * S::kBox + at * 128, nc + 64 * b, row);
+                            if (b < nb) load(mx, x + b * S::kBox + at * 128, nc + 64 * b, row);
                     };
                     // a partial block: its first 16 rows if that is all, else 64 at once
                     // (what lies behind the zeros is loaded and not multiplied)
@@ -196,7 +206,7 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
                     if (leader)
                         mbar_arrive_expect_tx(
                             &bk.full[stage],
-                            static_cast<uint32_t>(kCtas * (2 + S::kBBoxes) * 128 * loaded));
+                            static_cast<uint32_t>(kCtas * (2 + nb) * 128 * loaded));
                     if (left == ROWS) {
                         rows(&tmZ, &tmX, 0, row0 + r);
                     } else {
@@ -209,7 +219,7 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
                     issued = true;
                     pending |= 1u << stage;
                     pending_phase = (pending_phase & ~(1u << stage)) | (phase << stage);
-                    if (++stage == STAGES) {
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -217,7 +227,7 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
             }
             if (!ok && issued) {
                 if (leader) {
-                    for (int s = 0; s < STAGES; ++s)
+                    for (int s = 0; s < stages; ++s)
                         if (pending & (1u << s)) drain_wait(&bk.full[s], (pending_phase >> s) & 1u);
                 } else {
                     short_pause_ns(2000000ull);  // its copies complete on the leader's barriers
@@ -240,13 +250,14 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
                 }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kN);
+                const uint32_t idesc = idesc_bf16_f32_major(kM * kCtas, width_of(n0), true, true);
                 for (int r = 0; r < n; r += ROWS) {
                     if (!mbar_wait_asleep(&bk.full[stage], phase, abort_flag, args.status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t z = smem_u32(smem + stage * S::kStageBytes);
+                    const uint32_t z = smem_u32(smem + stage * stage_bytes);
                     const uint64_t zd = sw128_mn_desc(z, S::kBox);
                     const uint64_t xd = sw128_mn_desc(z + S::kABytes, S::kBox);
                     const int left = n - r;
@@ -255,9 +266,9 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
                         const uint32_t accumulate = (r != 0 || k != 0) ? 1u : 0u;
                         if (PAIR)
                             umma_bf16_pair(d_tmem, zd + kMnDescStep * k, xd + kMnDescStep * k,
-                                           kIdesc, accumulate);
+                                           idesc, accumulate);
                         else
-                            umma_bf16(d_tmem, zd + kMnDescStep * k, xd + kMnDescStep * k, kIdesc,
+                            umma_bf16(d_tmem, zd + kMnDescStep * k, xd + kMnDescStep * k, idesc,
                                       accumulate);
                     }
                     if (PAIR)
@@ -265,7 +276,7 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
                     else
                         umma_commit(&bk.empty[stage]);
                     issued = true;
-                    if (++stage == STAGES) {
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -309,7 +320,7 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
             constexpr int kCols = 128 / kEl;  // output columns per chunk
             const size_t row_bytes = static_cast<size_t>(args.N) * kEl;
 #pragma unroll 1
-            for (int c = group * kCols; c < kN; c += GROUPS * kCols) {
+            for (int c = group * kCols; c < args.width; c += GROUPS * kCols) {
                 uint4 out[8];  // this lane's row of the chunk
                 if (n == 0) {
 #pragma unroll
@@ -388,7 +399,7 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
 }
 
 template <bool PAIR, bool F32, int ROWS, int STAGES, int GROUPS>
-cudaError_t launch_wgrad(const LinearBwdArgs& a) {
+cudaError_t launch_wgrad(const LinearBwdArgs& a, int width) {
     constexpr int kCtas = PAIR ? 2 : 1;
     constexpr int kSmem = Shape<PAIR, ROWS, STAGES, GROUPS>::kSmem;
     constexpr int kThreads = Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads;
@@ -414,7 +425,8 @@ cudaError_t launch_wgrad(const LinearBwdArgs& a) {
     g.M = a.N;
     g.N = a.K;
     g.m_tiles = (a.N + kM * kCtas - 1) / (kM * kCtas);
-    g.n_tiles = (a.K + kN - 1) / kN;
+    g.width = width;
+    g.n_tiles = (a.K + width - 1) / width;
     g.out = a.dW;
     g.status = a.status;
     const long long tiles = static_cast<long long>(a.E) * g.m_tiles * g.n_tiles;
@@ -437,27 +449,70 @@ cudaError_t launch_wgrad(const LinearBwdArgs& a) {
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-// Average rows per group from which a pair of SMs shares a tile, if there is a tile for
-// every pair.  Measured at K = 4096, N = 14336, 8 experts, bf16: 32 rows a group 162 us on
-// single SMs and 182 on pairs, 64 rows 199 and 184, 128 rows 213 and 201, 256 rows 313 and
-// 268; one group of 2000 rows with K = N = 1024 (16 tiles of 256 x 256) 25 and 30.
-constexpr int kPairRowsPerGroup = 64;
+// Average rows per group below which a bf16 gradient is bound by its epilogue.
+constexpr int kShortRows = 64;
+
+struct Layout {
+    bool pair;
+    int width;
+};
+
+// The layout with the least clocks (as in grouped_linear_sm100.cu; fitted likewise) for groups of
+// the average size, the gradient's bytes to HBM being a floor for all; of layouts at the floor the
+// first wins.  Measured, zero data (us; pairs, then single SMs with 256, 128 and 64 inputs):
+//   8 groups, 256 rows, K 4096, N 14336, bf16     182  168  231  384   (sixteen epilogue warps)
+//   8 groups, 1024 rows, K 4096, N 14336, bf16    194  201  239  371
+//   8 groups, 8192 rows, K 4096, N 14336, bf16    554  641  777 1140
+//   8 groups, 512 rows, K 4096, N 14336, fp32     338  341  317  404
+//   1 group, 2000 rows, K 1024, N 1024, bf16       19   16   13   14
+//   2 groups, 5814 rows, K 104, N 2640, bf16       27   29   29   24
+//   1 group, 8000 rows, K 256, N 256, bf16         45   42   27   25
+Layout choose_layout(const LinearBwdArgs& a, int el) {
+    const int sms = device_sm_count();
+    const int n = a.rows < a.E ? 1 : a.rows / a.E;
+    const float floor = static_cast<float>(a.E) * a.N * a.K * el / (23.f * sms);
+    const float row_z = a.N % 64 == 0 ? 1.6f : 4.1f, row_x = a.K % 64 == 0 ? 1.6f : 4.1f;
+    Layout best{false, kN};
+    float least = 0.f;
+    auto offer = [&](bool pair, int width) {
+        const int ctas = pair ? 2 : 1;
+        const long long tiles = static_cast<long long>(a.E) * ((a.N + kM * ctas - 1) / (kM * ctas)) *
+                                ((a.K + width - 1) / width);
+        const long long rounds = (tiles + sms / ctas - 1) / (sms / ctas);
+        const int wide = a.K < width ? (a.K + 31) / 32 * 32 : width;
+        const float boxes = static_cast<float>((wide / ctas + 63) / 64);
+        const float load = 64.f * (2.f * row_z + boxes * row_x);
+        const float block = fmaxf(fmaxf(2.02f * wide, 260.f + 1.1f * wide), load);
+        const float products = static_cast<float>((n + 63) / 64) * block;
+        const float epilogue = el == 2 ? 1200.f + 7.3f * wide : 24.5f * wide;
+        float clocks = static_cast<float>(rounds) * fmaxf(products, epilogue) + epilogue;
+        if (pair) clocks += 6500.f;
+        if (clocks < floor) clocks = floor;
+        if (least == 0.f || clocks < least) best = {pair, width}, least = clocks;
+    };
+    const bool pairs = n >= kShortRows && pair_gemm_enabled();
+    if (pairs && n >= 2 * kShortRows) offer(true, kN);
+    if (el == 4) offer(false, 128);
+    offer(false, kN);
+    if (el == 2) offer(false, 128);
+    offer(false, 64);
+    if (pairs && n < 2 * kShortRows) offer(true, kN);
+    return best;
+}
 
 template <bool F32>
 cudaError_t launch_typed(const LinearBwdArgs& a) {
-    const long long pair_tiles =
-        static_cast<long long>(a.E) * ((a.N + 255) / 256) * ((a.K + kN - 1) / kN);
-    if (a.rows / a.E >= kPairRowsPerGroup && pair_tiles >= device_sm_count() / 2 &&
-        pair_gemm_enabled()) {
-        const cudaError_t err = launch_wgrad<true, F32, 128, 3, 2>(a);
+    const Layout l = choose_layout(a, F32 ? 4 : 2);
+    if (l.pair) {
+        const cudaError_t err = launch_wgrad<true, F32, 128, 3, 2>(a, l.width);
         if (err == cudaSuccess || err == cudaErrorInvalidValue) return err;
         cudaGetLastError();  // no room for a pair of CTAs: single SMs
     }
     // Short reductions in bf16 are bound by the epilogue: sixteen warps of it (32 rows, as
     // above: 149 us against 169 with eight and four stages).  fp32 has half the values per
     // byte and twice the bytes, where more writers only scatter them (341 against 316 us).
-    if (!F32 && a.rows / a.E < kPairRowsPerGroup) return launch_wgrad<false, F32, 64, 2, 4>(a);
-    return launch_wgrad<false, F32, 64, 4, 2>(a);
+    if (!F32 && a.rows / a.E < kShortRows) return launch_wgrad<false, F32, 64, 2, 4>(a, l.width);
+    return launch_wgrad<false, F32, 64, 4, 2>(a, l.width);
 }
 
 }  // namespace

@@ -314,6 +314,18 @@ def test_backward(shape, dw_dtype):
             assert not bool(dW[e].any()) and not bool(db[e].any())
 
 
+# tiles of 64, 128 and 256 inputs, their last one narrower, and rows that lie across lines
+@pytest.mark.parametrize("dw_dtype", [bf, f32])
+@pytest.mark.parametrize("shape", [((2000,), 520, 1024), ((130, 900), 96, 1320),
+                                   ((1000, 24), 176, 392), ((70,), 2056, 2056),
+                                   ((257, 0, 640), 1032, 1288), ((3000,), 72, 24)], ids=ids)
+def test_backward_tile_widths(shape, dw_dtype):
+    counts, K, N = shape
+    t = R.inputs(counts, K, N, bf, 300 + K, tail=3)
+    dx, dW, db, zhat, *_ = run_backward(t, counts, "silu", dw_dtype, tail=3)
+    check_gradients(dx, dW, db, t, zhat, "silu", counts)
+
+
 @pytest.mark.parametrize("counts", [(5, 0, 20), (300, 260), (1100, 900)])
 @pytest.mark.parametrize("name", R.ACTS)
 def test_backward_every_activation_and_any_gradient_alone(counts, name):

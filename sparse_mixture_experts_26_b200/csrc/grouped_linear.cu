@@ -1,12 +1,14 @@
 // grouped_linear.cu -- the grouped linear operators' launches, and the fp32 forward on CUDA
 // cores (fp32 throughout, no TF32: y_r = act(x_r W_e^T + b_e) + residual_r).
 //
-// The fp32 kernel: 128 threads, 16 (rows) x 8 (features), each with RM x RN sums in
-// registers.  Steps of 32 of the reduction go through shared memory in rows of 36 floats, so
-// that every read is 16 bytes (RM + RN reads for 4 RM RN multiply-adds); the next step's
-// global loads are in flight meanwhile.  Small problems are chains of latencies and want
-// many small tiles, large ones the better ratio of multiply-adds to reads:
-// 32 x 32 tiles (2 x 4 sums) while 128 x 64 ones (8 x 8) would leave SMs without work.
+// The fp32 kernel: 128 threads, 16 (rows) x 8 (features), each with RM x RN sums in registers,
+// one over the even and one over the odd k of the reduction: a 16-byte read of either operand
+// then is two operands of an instruction that does two multiply-adds, with nothing to
+// rearrange.  Steps of 32 of the reduction come asynchronously into three stages of shared
+// memory, in rows of 36 floats, so that no read meets a bank twice; one barrier a step.
+// Small problems are chains of latencies and want many small tiles, large ones the better ratio
+// of multiply-adds to reads (launch_linear_f32).  Measured: 4096^3 47.6 TFLOP/s (cuBLAS 57),
+// 512 x 1024 -> 1024 38.6 us (scalar sums and two barriers a step: 34.5 TFLOP/s, 88 us).
 #include <cuda_bf16.h>
 
 #include "linear_device.cuh"
@@ -15,16 +17,29 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kStep = 32;            // reduction per step
+constexpr int kStep = 32;            // reduction per stage
 constexpr int kPitch = kStep + 4;    // floats
+constexpr int kStages = 3;
+
+template <int RM, int RN>
+struct F32Tile {
+    static constexpr int kRows = 16 * RM, kF = 8 * RN;
+    static constexpr int kStageFloats = (kRows + kF) * kPitch;
+    static constexpr int kSmem = kStages * kStageFloats * 4;
+};
+
+// 16 bytes global -> shared, asynchronously; zeros if !have.
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool have) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(have ? 16 : 0)
+                 : "memory");
+}
 
 template <int RM, int RN>
 __global__ void __launch_bounds__(kThreads) linear_f32_kernel(const LinearArgs a, int ftiles) {
-    constexpr int kRowTile = 16 * RM, kFTile = 8 * RN;
-    constexpr int kX = kRowTile * kStep / 4 / kThreads;  // 16-byte loads a thread and step
-    constexpr int kW = kFTile * kStep / 4 / kThreads;
+    using Tile = F32Tile<RM, RN>;
+    extern __shared__ __align__(16) float smem_f32[];
     __shared__ int off[kMaxExperts + 1];
-    __shared__ __align__(16) float sx[kRowTile * kPitch], sw[kFTile * kPitch];
     pdl_wait();
     pdl_launch_dependents();
     if (threadIdx.x < 32) load_group_bounds(a.offsets, a.E, a.rows, off);
@@ -32,69 +47,75 @@ __global__ void __launch_bounds__(kThreads) linear_f32_kernel(const LinearArgs a
     int ft;
     int y = divide(blockIdx.x, ftiles, ft), e = 0;  // row tile y of all groups'
     for (; e < a.E; ++e) {
-        const int t = (off[e + 1] - off[e] + kRowTile - 1) / kRowTile;
+        const int t = (off[e + 1] - off[e] + Tile::kRows - 1) / Tile::kRows;
         if (y < t) break;
         y -= t;
     }
     if (e == a.E) return;
-    const int row0 = off[e] + y * kRowTile, row_end = off[e + 1], f0 = ft * kFTile;
+    const int row0 = off[e] + y * Tile::kRows, row_end = off[e + 1], f0 = ft * Tile::kF;
     const float* __restrict__ x = static_cast<const float*>(a.x);
     const float* __restrict__ W =
         static_cast<const float*>(a.W) + static_cast<size_t>(e) * a.N * a.K;
     const int part = threadIdx.x & 7, line = threadIdx.x >> 3;  // loads: 8 threads a row
     const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
 
-    float4 px[kX], pw[kW];
-    auto fetch = [&](int k0) {
-        const int k = k0 + part * 4;
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int steps = (a.K + kStep - 1) / kStep;
+    auto fetch = [&](int step) {
+        if (step < steps) {
+            const int k = step * kStep + part * 4;
+            float* sx = smem_f32 + step % kStages * Tile::kStageFloats + line * kPitch + part * 4;
+            float* sw = sx + Tile::kRows * kPitch;
 #pragma unroll
-        for (int i = 0; i < kX; ++i) {
-            const int r = row0 + line + 16 * i;
-            px[i] = r < row_end && k < a.K
-                        ? *reinterpret_cast<const float4*>(x + static_cast<size_t>(r) * a.K + k)
-                        : zero;
-        }
+            for (int i = 0; i < Tile::kRows / 16; ++i) {
+                const int r = row0 + line + 16 * i;
+                const bool have = r < row_end && k < a.K;
+                copy16(sx + 16 * i * kPitch, have ? x + static_cast<size_t>(r) * a.K + k : x, have);
+            }
 #pragma unroll
-        for (int i = 0; i < kW; ++i) {
-            const int f = f0 + line + 16 * i;
-            pw[i] = f < a.N && k < a.K
-                        ? *reinterpret_cast<const float4*>(W + static_cast<size_t>(f) * a.K + k)
-                        : zero;
+            for (int i = 0; i < Tile::kF / 16; ++i) {
+                const int f = f0 + line + 16 * i;
+                const bool have = f < a.N && k < a.K;
+                copy16(sw + 16 * i * kPitch, have ? W + static_cast<size_t>(f) * a.K + k : W, have);
+            }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    float acc[RM][RN] = {};
-    fetch(0);
-    for (int k0 = 0; k0 < a.K; k0 += kStep) {
-        __syncthreads();
+    F2 pair[RM][RN] = {};  // sums over even and over odd k
 #pragma unroll
-        for (int i = 0; i < kX; ++i)
-            *reinterpret_cast<float4*>(sx + (line + 16 * i) * kPitch + part * 4) = px[i];
-#pragma unroll
-        for (int i = 0; i < kW; ++i)
-            *reinterpret_cast<float4*>(sw + (line + 16 * i) * kPitch + part * 4) = pw[i];
-        __syncthreads();
-        if (k0 + kStep < a.K) fetch(k0 + kStep);
+    for (int s = 0; s < kStages - 1; ++s) fetch(s);
+    for (int step = 0; step < steps; ++step) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncthreads();  // this step's values are there, the last step's have been read
+        fetch(step + kStages - 1);
+        const float* sx = smem_f32 + step % kStages * Tile::kStageFloats + ty * kPitch;
+        const float* sw = smem_f32 + step % kStages * Tile::kStageFloats +
+                          (Tile::kRows + tx) * kPitch;
 #pragma unroll
         for (int k = 0; k < kStep; k += 4) {
-            float4 xv[RM], wv[RN];
+            ulonglong2 xv[RM];
 #pragma unroll
             for (int i = 0; i < RM; ++i)
-                xv[i] = *reinterpret_cast<const float4*>(sx + (ty + 16 * i) * kPitch + k);
+                xv[i] = *reinterpret_cast<const ulonglong2*>(sx + 16 * i * kPitch + k);
 #pragma unroll
-            for (int j = 0; j < RN; ++j)
-                wv[j] = *reinterpret_cast<const float4*>(sw + (tx + 8 * j) * kPitch + k);
+            for (int j = 0; j < RN; ++j) {
+                const ulonglong2 wv = *reinterpret_cast<const ulonglong2*>(sw + 8 * j * kPitch + k);
 #pragma unroll
-            for (int i = 0; i < RM; ++i)
-#pragma unroll
-                for (int j = 0; j < RN; ++j) {
-                    acc[i][j] = fmaf(xv[i].x, wv[j].x, acc[i][j]);
-                    acc[i][j] = fmaf(xv[i].y, wv[j].y, acc[i][j]);
-                    acc[i][j] = fmaf(xv[i].z, wv[j].z, acc[i][j]);
-                    acc[i][j] = fmaf(xv[i].w, wv[j].w, acc[i][j]);
+                for (int i = 0; i < RM; ++i) {
+                    pair[i][j] = f2_fma(xv[i].x, wv.x, pair[i][j]);
+                    pair[i][j] = f2_fma(xv[i].y, wv.y, pair[i][j]);
                 }
+            }
         }
     }
+    float acc[RM][RN];
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int j = 0; j < RN; ++j) {
+            float even, odd;
+            f2_get(pair[i][j], even, odd);
+            acc[i][j] = even + odd;
+        }
     // eight of a thread's outputs at a time; features 8 apart, so eight lanes write 32 bytes
     const float* bias = static_cast<const float*>(a.bias);
     const float* residual = static_cast<const float*>(a.residual);
@@ -121,20 +142,51 @@ __global__ void __launch_bounds__(kThreads) linear_f32_kernel(const LinearArgs a
 }
 
 template <int RM, int RN>
-cudaError_t launch_f32(const LinearArgs& a, long long& blocks, bool go) {
-    const int ftiles = (a.N + 8 * RN - 1) / (8 * RN);
+long long f32_blocks(const LinearArgs& a) {
+    using Tile = F32Tile<RM, RN>;
     const int groups = a.rows < a.E ? a.rows : a.E;
-    blocks = (a.rows / (16 * RM) + groups) * static_cast<long long>(ftiles);
-    if (!go) return cudaSuccess;
-    return launch_k(linear_f32_kernel<RM, RN>, static_cast<unsigned>(blocks), kThreads, 0, a.stream,
-                    a, ftiles);
+    return (a.rows / Tile::kRows + groups) *
+           static_cast<long long>((a.N + Tile::kF - 1) / Tile::kF);
 }
 
+template <int RM, int RN>
+cudaError_t launch_f32(const LinearArgs& a) {
+    using Tile = F32Tile<RM, RN>;
+    static PerDeviceOnce once;
+    if (const cudaError_t err = opt_in_smem(once, linear_f32_kernel<RM, RN>, Tile::kSmem);
+        err != cudaSuccess)
+        return err;
+    return launch_k(linear_f32_kernel<RM, RN>, static_cast<unsigned>(f32_blocks<RM, RN>(a)), kThreads,
+                    Tile::kSmem, a.stream, a, (a.N + Tile::kF - 1) / Tile::kF);
+}
+
+// Clocks of a step: a block's own latency, or its SM's throughput.
+template <int RM, int RN>
+float f32_clocks(const LinearArgs& a, float latency, float throughput) {
+    using Tile = F32Tile<RM, RN>;
+    const int groups = a.rows < a.E ? a.rows : a.E;
+    const int n = (a.rows + groups - 1) / groups;
+    const long long blocks = static_cast<long long>(groups) *
+                             ((n + Tile::kRows - 1) / Tile::kRows) *
+                             ((a.N + Tile::kF - 1) / Tile::kF);
+    const long long sms = device_sm_count();
+    const float busy = static_cast<float>((blocks + sms - 1) / sms) * throughput;
+    return latency > busy ? latency : busy;
+}
+
+// Measured (us; tiles of 32 x 32, 64 x 32 and 128 x 64; the clocks are fitted to these):
+//   1 group, 1 row, K 1024, N 1024         17    26    57
+//   1 group, 256 rows, K 1024, N 1024      27    28    61
+//   1 group, 512 rows, K 1024, N 1024      75    39    62
+//   8 groups, 1024 rows, K 1024, N 1024    83    68   109
+//   32 groups, 1000 rows, K 512, N 768     43    51    81
+//   1 group, 4096 rows, K 4096, N 4096   4980  3480  2890
 cudaError_t launch_linear_f32(const LinearArgs& a) {
-    long long blocks;
-    launch_f32<8, 8>(a, blocks, false);
-    return blocks >= 2LL * device_sm_count() ? launch_f32<8, 8>(a, blocks, true)
-                                             : launch_f32<2, 4>(a, blocks, true);
+    const float small = f32_clocks<2, 4>(a, 985.f, 670.f);
+    const float middle = f32_clocks<4, 4>(a, 1550.f, 930.f);
+    const float large = f32_clocks<8, 8>(a, 6500.f, 3100.f);
+    if (small <= middle && small <= large) return launch_f32<2, 4>(a);
+    return middle <= large ? launch_f32<4, 4>(a) : launch_f32<8, 8>(a);
 }
 
 }  // namespace

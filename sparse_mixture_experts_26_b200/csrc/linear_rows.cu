@@ -8,13 +8,14 @@
 //
 // Bytes: dy 2, code 1.125, dz 2 per value; 25 instructions a value (GELU) weigh as much.  A
 // block takes 256 columns of a chunk of 64 to 512 rows of one group: a warp reads 512 bytes of
-// a row, eight columns a lane, and the eight warps take the rows in turn, two in flight a
-// thread.  The warps' column sums are added in order in shared memory; the chunks' go to the
-// workspace, and the block that brings a group's last chunk adds them in chunk order
+// a row, eight columns a lane, and the eight warps take the rows in turn, two (or four) in
+// flight a thread.  The warps' column sums are added in order in shared memory; the chunks' go
+// to the workspace, and the block that brings a group's last chunk adds them in chunk order
 // (whichever block that is, so db does not depend on the timing).  Without an activation dz
 // is dy itself: only the tails and db are made.
-// Measured at 8192 x 14336 with db (us; 600 MB): ReLU 119, SiLU 128, GELU 139; with chunks of
-// 64 rows 131, 142 and 160.
+// Measured at 8192 x 14336 with db (us; 600 MB): ReLU 117, SiLU 127, GELU 134; with chunks of
+// 64 rows 131, 142 and 160.  Small calls: one warp finds all groups' chunks with a scan (a walk
+// over the groups by every thread took 250 clocks a group: 32 groups, 150 x 144, 5.9 -> 2.4 us).
 #include <cuda_bf16.h>
 
 #include "linear_device.cuh"
@@ -46,20 +47,38 @@ struct DzArgs {
     int n_strips;
 };
 
+struct Groups {
+    int off[kMaxExperts + 1];
+    int chunk[kMaxExperts + 1];  // groups' first chunks; an empty group has one too
+};
+// One warp fills them.
+__device__ __forceinline__ void load_groups(const DzArgs& a, Groups& g) {
+    const int lane = threadIdx.x & 31;
+    load_group_bounds(a.offsets, a.E, a.rows, g.off);
+    int rest, sum = 0;
+    if (lane < a.E)
+        sum = max(divide(g.off[lane + 1] - g.off[lane] + a.chunk_rows - 1, a.chunk_rows, rest), 1);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int below = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += below;
+    }
+    if (lane < a.E) g.chunk[lane + 1] = sum;
+    if (lane == 0) g.chunk[0] = 0;
+}
+
 // One chunk's strip of columns.  All threads of the block call this together.
-__device__ __forceinline__ void dz_item(const DzArgs& a, const int* off, float (*s_sum)[kCols],
-                                        int& s_last, int item) {
+template <int FLIGHT>
+__device__ __forceinline__ void dz_item(const DzArgs& a, const Groups& groups,
+                                        float (*s_sum)[kCols], int& s_last, int item) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int* off = groups.off;
     int strip;
     const int chunk = divide(item, a.strips, strip);
-    int e = 0, i = chunk, chunks = 0;  // chunk i of group e's; an empty group has one too
-    for (; e < a.E; ++e) {
-        int rest;
-        chunks = max(divide(off[e + 1] - off[e] + a.chunk_rows - 1, a.chunk_rows, rest), 1);
-        if (i < chunks) break;
-        i -= chunks;
-    }
+    const int e = __popc(__ballot_sync(0xffffffffu, lane < a.E && groups.chunk[lane + 1] <= chunk));
     if (e == a.E) return;
+    const int i = chunk - groups.chunk[e];  // chunk i of the group's
+    const int chunks = groups.chunk[e + 1] - groups.chunk[e];
     const int of_group = off[e + 1] - off[e];
     const int first = i * a.chunk_rows;             // this chunk's rows, counted in the group
     const int end = min(first + a.chunk_rows, of_group);
@@ -88,13 +107,12 @@ __device__ __forceinline__ void dz_item(const DzArgs& a, const int* off, float (
     const int nb = ckpt_blocks(a.N);
     float sum[8] = {};
     if (have) {
-        constexpr int kFlight = 2;  // rows whose loads are in flight together
-        for (int r0 = first + warp; r0 < end; r0 += kFlight * kWarps) {
-            uint4 dy[kFlight];
-            uint2 q[kFlight];
-            float s[kFlight];
+        for (int r0 = first + warp; r0 < end; r0 += FLIGHT * kWarps) {
+            uint4 dy[FLIGHT];  // rows whose loads are in flight together
+            uint2 q[FLIGHT];
+            float s[FLIGHT];
 #pragma unroll
-            for (int k = 0; k < kFlight; ++k) {
+            for (int k = 0; k < FLIGHT; ++k) {
                 const int r = r0 + k * kWarps;
                 if (r >= end) continue;
                 const size_t row = static_cast<size_t>(row0 + r), at = row * a.N + c;
@@ -105,7 +123,7 @@ __device__ __forceinline__ void dz_item(const DzArgs& a, const int* off, float (
                 }
             }
 #pragma unroll
-            for (int k = 0; k < kFlight; ++k) {
+            for (int k = 0; k < FLIGHT; ++k) {
                 const int r = r0 + k * kWarps;
                 if (r >= end) continue;
                 float g[8] = {bf16_lo(dy[k].x), bf16_hi(dy[k].x), bf16_lo(dy[k].y),
@@ -145,16 +163,17 @@ __device__ __forceinline__ void dz_item(const DzArgs& a, const int* off, float (
         return;
     }
     if (col < a.N) __stcg(a.part + static_cast<size_t>(chunk) * a.N + col, total);
-    __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
+        // the barriers carry the block's stores to this fence, and what it sees to the block
+        __threadfence();
         uint32_t* counter = a.counters + static_cast<size_t>(e) * a.n_strips + strip;
         s_last = atomicAdd(counter, 1u) == static_cast<uint32_t>(chunks - 1);
         if (s_last) *counter = 0;  // zero again for the next call
+        __threadfence();
     }
     __syncthreads();
     if (!s_last) return;
-    __threadfence();
     // warp w adds chunks w, w + 8, .. of the group, then the warps' sums are added
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum[k] = 0.f;
@@ -172,14 +191,17 @@ __device__ __forceinline__ void dz_item(const DzArgs& a, const int* off, float (
     if (col < a.N) *db = total;
 }
 
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) linear_dz_kernel(const DzArgs a) {
-    __shared__ int off[kMaxExperts + 1], s_last;
+template <int FLIGHT, int BLOCKS_PER_SM>
+__global__ void __launch_bounds__(kThreads, BLOCKS_PER_SM) linear_dz_kernel(const DzArgs a) {
+    __shared__ Groups groups;
+    __shared__ int s_last;
     __shared__ __align__(16) float s_sum[kWarps][kCols];  // written 16 bytes at a time
     pdl_wait();
     pdl_launch_dependents();
-    if (threadIdx.x < 32) load_group_bounds(a.offsets, a.E, a.rows, off);
+    if (threadIdx.x < 32) load_groups(a, groups);
     __syncthreads();
-    for (int item = blockIdx.x; item < a.items; item += gridDim.x) dz_item(a, off, s_sum, s_last, item);
+    for (int item = blockIdx.x; item < a.items; item += gridDim.x)
+        dz_item<FLIGHT>(a, groups, s_sum, s_last, item);
 }
 
 }  // namespace
@@ -220,7 +242,11 @@ cudaError_t launch_linear_dz(const LinearBwdArgs& a) {
         }
     }
     d.items = static_cast<int>(chunks * d.strips);  // rows * N, rows * K < 2^40: below 2^31
-    return launch_k(linear_dz_kernel, d.items < blocks ? d.items : blocks, kThreads, 0, a.stream, d);
+    // Few items are chains of latencies: four rows in flight where two blocks an SM hold them all
+    // (164 x 176 6.9 -> 6.1 us, 1616 x 824 7.8 -> 7.2; but 8192 x 14336 134 -> 155).
+    if (d.items <= 2 * device_sm_count())
+        return launch_k(linear_dz_kernel<4, 2>, d.items, kThreads, 0, a.stream, d);
+    return launch_k(linear_dz_kernel<2, kBlocksPerSm>, d.items < blocks ? d.items : blocks, kThreads, 0, a.stream, d);
 }
 
 }  // namespace moe

@@ -613,7 +613,13 @@ def moe_grouped_linear_train(x, offsets, W, y, codes, scales, ws, bias=None, res
 
 def grouped_linear(x, offsets, W, bias=None, residual=None, act: str = "none", ws=None, out=None,
                    stream=None) -> torch.Tensor:
-    """``moe_grouped_linear``, allocating the workspace and output with torch if not given."""
+    """``moe_grouped_linear``, allocating the workspace and output with torch if not given (on
+    ``stream``, so that both are zeroed and reused in its order)."""
+    if stream is not None and (ws is None or out is None):
+        side = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(
+            int(stream), x.device)
+        with torch.cuda.stream(side):
+            return grouped_linear(x, offsets, W, bias, residual, act, ws, out)
     if ws is None:
         ws = alloc_grouped_linear_workspace(x.shape[0], x.shape[1], W.shape[1], W.shape[0],
                                             x.dtype, x.device)

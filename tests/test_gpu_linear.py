@@ -525,6 +525,24 @@ def test_two_streams_with_a_workspace_each():
         check_y(y, t, counts, K, "gelu", 90)
 
 
+def test_allocating_call_on_a_given_stream():
+    """The workspace that the call allocates is zeroed, and later handed on, in the order of the
+    stream it is used on: the current stream is busy meanwhile, its cached blocks hold ones."""
+    K, N = 4096, 1032
+    t = R.inputs((3,), K, N, bf, 77)
+    need = moe.moe_grouped_linear_workspace_bytes(3, K, N, 1)
+    for side in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        dirty = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        del dirty
+        torch.cuda._sleep(50_000_000)  # some 30 ms
+        y = moe.grouped_linear(t["x"], None, t["W"], t["bias"], act="gelu", stream=side)
+        noise = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        check_y(y, t, (3,), K, "gelu", 3)
+        del noise
+
+
 def test_four_threads_call_at_once():
     """Own streams and workspaces, the first calls of their shapes: equal to serial calls."""
     import threading

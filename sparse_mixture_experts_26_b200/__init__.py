@@ -524,90 +524,96 @@ def alloc_checkpoint(rows: int, N: int, device="cuda"):
             torch.empty(rows, nb, dtype=torch.float32, device=device))
 
 
-# The checks below cost as much as a small kernel, so each compares in place and calls
-# _expect, which words the error, only when it fails.
+# The checks below cost as much as a small kernel, so each compares in place, in few calls,
+# and asks _expect and _dev, which word the error, only when one fails.
 def _check_checkpoint(codes, scales, rows: int, N: int) -> None:
-    if codes.shape != (rows, N) or codes.dtype != torch.int8:
+    if codes.shape != (rows, N) or codes.dtype is not torch.int8:
         _expect("codes", codes, (rows, N), torch.int8)
     nb = (N + CHECKPOINT_BLOCK - 1) // CHECKPOINT_BLOCK
-    if scales.shape != (rows, nb) or scales.dtype != torch.float32:
+    if scales.shape != (rows, nb) or scales.dtype is not torch.float32:
         _expect("scales", scales, (rows, nb), torch.float32)
 
 
-def _call(fn: str, tensors, stream, *args) -> None:
-    """Call ``fn(*args, stream)`` under the tensors' device: switched only if another one is
+_get_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _call(f, tensors, stream, *args) -> None:
+    """Call ``f(*args, stream)`` under the tensors' device: switched only if another one is
     current, and the current stream read as a bare handle."""
-    first = tensors[0]
-    index = first.get_device()
+    index = tensors[0].get_device()
     for t in tensors:
         if t is not None and (t.get_device() != index or index < 0 or not t.is_contiguous()):
             _dev(*[t for t in tensors if t is not None])  # says what is wrong
-    f = getattr(_lib, fn)
-    if torch.cuda.current_device() == index:
-        code = f(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None
-                 else _stream(stream))
+    if _get_device() == index:
+        code = f(*args, _raw_stream(index) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(index):
             code = f(*args, _stream(stream))
     if code:
-        _check(fn, code)
+        _check(f.__name__, code)
 
 
 _DTYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
 
 
 def _linear_dims(x, offsets, W, bias):
-    if x.dim() != 2 or W.dim() != 3:
-        raise ValueError("x must be [rows, K] and W [E, N, K]")
-    rows, K = x.shape
-    E, N, K_w = W.shape
+    try:
+        rows, K = x.shape
+        E, N, K_w = W.shape
+    except ValueError:
+        raise ValueError("x must be [rows, K] and W [E, N, K]") from None
     dtype = x.dtype
     dt = _DTYPES.get(dtype)
     if dt is None:
         _dt(x)
-    if K_w != K or W.dtype != dtype:
+    if K_w != K or W.dtype is not dtype:
         _expect("W", W, (E, N, K), dtype)
     if offsets is None:
         if E != 1:
             raise ValueError("offsets may be None only with one expert")
-    elif offsets.numel() != E + 1 or offsets.dtype != torch.int32:
+    elif offsets.numel() != E + 1 or offsets.dtype is not torch.int32:
         _expect_numel("offsets", offsets, E + 1, torch.int32)
-    if bias is not None and (bias.shape != (E, N) or bias.dtype != dtype):
+    if bias is not None and (bias.shape != (E, N) or bias.dtype is not dtype):
         _expect("bias", bias, (E, N), dtype)
     return rows, K, N, E, dt
 
 
-def _linear(fn, x, offsets, W, y, ws, bias, residual, act, codes, scales, stream) -> None:
+def _linear(f, x, offsets, W, y, ws, bias, residual, act, codes, scales, stream) -> None:
     rows, K, N, E, dt = _linear_dims(x, offsets, W, bias)
     if y.shape != (rows, N):
         _expect("y", y, (rows, N))
     y_dt = _DTYPES.get(y.dtype)
     if y_dt is None:
         _dt(y)
-    if residual is not None and (residual.shape != (rows, N) or residual.dtype != x.dtype):
+    if residual is not None and (residual.shape != (rows, N) or residual.dtype is not x.dtype):
         _expect("residual", residual, (rows, N), x.dtype)
-    _ws("ws", ws)
-    kept = () if codes is None else (codes.data_ptr(), scales.data_ptr())
-    _call(fn, (x, offsets, W, y, ws, bias, residual, codes, scales), stream,
-          x.data_ptr(), _ptr(offsets), W.data_ptr(), _ptr(bias), _ptr(residual), rows, K, N, E,
-          _ACTS[act] if act in _ACTS else _act(act), dt, y_dt, y.data_ptr(), *kept,
-          ws.data_ptr(), ws.numel())
+    if ws.dtype is not torch.uint8 or ws.dim() != 1:
+        _ws("ws", ws)
+    args = (x.data_ptr(), None if offsets is None else offsets.data_ptr(), W.data_ptr(),
+            None if bias is None else bias.data_ptr(),
+            None if residual is None else residual.data_ptr(), rows, K, N, E,
+            _ACTS[act] if act in _ACTS else _act(act), dt, y_dt, y.data_ptr())
+    if codes is None:
+        _call(f, (x, offsets, W, y, ws, bias, residual), stream, *args, ws.data_ptr(), ws.numel())
+    else:
+        _check_checkpoint(codes, scales, rows, N)
+        _call(f, (x, offsets, W, y, ws, bias, residual, codes, scales), stream, *args,
+              codes.data_ptr(), scales.data_ptr(), ws.data_ptr(), ws.numel())
 
 
 def moe_grouped_linear(x, offsets, W, y, ws, bias=None, residual=None, act: str = "none",
                        stream=None) -> None:
     """``y_r = act(x_r W_e^T + b_e) + residual_r`` for every row r of expert e's group.
     ``offsets`` may be None with one expert; ``act`` is "none", "relu", "gelu" or "silu"."""
-    _linear("moe_grouped_linear", x, offsets, W, y, ws, bias, residual, act, None, None, stream)
+    _linear(_lib.moe_grouped_linear, x, offsets, W, y, ws, bias, residual, act, None, None, stream)
 
 
 def moe_grouped_linear_train(x, offsets, W, y, codes, scales, ws, bias=None, residual=None,
                              act: str = "none", stream=None) -> None:
     """``moe_grouped_linear`` that also keeps the pre-activation in 8 bits (``codes``,
     ``scales`` as from ``alloc_checkpoint``) for ``moe_grouped_linear_backward``."""
-    if x.dim() == 2 and W.dim() == 3:
-        _check_checkpoint(codes, scales, x.shape[0], W.shape[1])
-    _linear("moe_grouped_linear_train", x, offsets, W, y, ws, bias, residual, act, codes, scales,
+    _linear(_lib.moe_grouped_linear_train, x, offsets, W, y, ws, bias, residual, act, codes, scales,
             stream)
 
 
@@ -635,9 +641,11 @@ def moe_checkpoint_save(v, codes, scales, stream=None) -> None:
         raise ValueError("v must be [rows, N]")
     rows, N = v.shape
     _check_checkpoint(codes, scales, rows, N)
-    dt = _dt(v)
-    _call("moe_checkpoint_save", (v, codes, scales), stream,
-          _ptr(v), rows, N, dt, _ptr(codes), _ptr(scales))
+    dt = _DTYPES.get(v.dtype)
+    if dt is None:
+        _dt(v)
+    _call(_lib.moe_checkpoint_save, (v, codes, scales), stream,
+          v.data_ptr(), rows, N, dt, codes.data_ptr(), scales.data_ptr())
 
 
 def moe_checkpoint_restore(codes, scales, out, act: str = "none", stream=None) -> None:
@@ -646,9 +654,12 @@ def moe_checkpoint_restore(codes, scales, out, act: str = "none", stream=None) -
         raise ValueError("out must be [rows, N]")
     rows, N = out.shape
     _check_checkpoint(codes, scales, rows, N)
-    dt = _dt(out)
-    _call("moe_checkpoint_restore", (codes, scales, out), stream,
-          _ptr(codes), _ptr(scales), rows, N, _act(act), dt, _ptr(out))
+    dt = _DTYPES.get(out.dtype)
+    if dt is None:
+        _dt(out)
+    _call(_lib.moe_checkpoint_restore, (codes, scales, out), stream,
+          codes.data_ptr(), scales.data_ptr(), rows, N, _ACTS[act] if act in _ACTS else _act(act),
+          dt, out.data_ptr())
 
 
 def moe_grouped_linear_backward(dy, x, offsets, W, ws, dx=None, dW=None, db=None, codes=None,
@@ -657,22 +668,25 @@ def moe_grouped_linear_backward(dy, x, offsets, W, ws, dx=None, dW=None, db=None
     (x's dtype), ``dW`` (bf16 or fp32) and ``db`` (fp32) that is given is overwritten.
     ``codes`` and ``scales`` may be left out with ``act="none"``."""
     rows, K, N, E, dt = _linear_dims(x, offsets, W, None)
-    if dy.shape != (rows, N) or dy.dtype != x.dtype:
+    if dy.shape != (rows, N) or dy.dtype is not x.dtype:
         _expect("dy", dy, (rows, N), x.dtype)
-    if dx is not None and (dx.shape != (rows, K) or dx.dtype != x.dtype):
+    if dx is not None and (dx.shape != (rows, K) or dx.dtype is not x.dtype):
         _expect("dx", dx, (rows, K), x.dtype)
     dw_dt = dt
     if dW is not None:
         if dW.shape != W.shape:
             _expect("dW", dW, (E, N, K))
-        dw_dt = _dt(dW)
-    if db is not None and (db.shape != (E, N) or db.dtype != torch.float32):
+        dw_dt = _DTYPES.get(dW.dtype)
+        if dw_dt is None:
+            _dt(dW)
+    if db is not None and (db.shape != (E, N) or db.dtype is not torch.float32):
         _expect("db", db, (E, N), torch.float32)
     if (codes is None) != (scales is None):
         raise ValueError("codes and scales go together")
     if codes is not None:
         _check_checkpoint(codes, scales, rows, N)
-    _ws("ws", ws)
-    _call("moe_grouped_linear_backward", (dy, x, offsets, W, ws, dx, dW, db, codes, scales),
+    if ws.dtype is not torch.uint8 or ws.dim() != 1:
+        _ws("ws", ws)
+    _call(_lib.moe_grouped_linear_backward, (dy, x, offsets, W, ws, dx, dW, db, codes, scales),
           stream, _ptr(dy), _ptr(x), _ptr(offsets), _ptr(W), _ptr(codes), _ptr(scales), rows, K,
           N, E, _act(act), dt, dw_dt, _ptr(dx), _ptr(dW), _ptr(db), _ptr(ws), ws.numel())

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads)
             const int r = w.row + d + k * w.step;
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[k][i] = 0.f;
-            if (have && r < rows) load8(v + static_cast<size_t>(r) * N + w.c, x[k]);
+            if (have && r < rows) load8_global(v + static_cast<size_t>(r) * N + w.c, x[k]);
         }
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 6)
             float x[8];
             ckpt_unpack8(q[k], s[k], x);
             act_value8(act, x);
-            store8(out + static_cast<size_t>(r) * N + w.c, x);
+            store8_global(out + static_cast<size_t>(r) * N + w.c, x);
         }
     }
 }

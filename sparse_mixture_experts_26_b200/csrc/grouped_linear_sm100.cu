@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v[6] += bf16_lo(res.w), v[7] += bf16_hi(res.w);
                 }
                 if (args.out_f32)
-                    store8(static_cast<float*>(args.out) + at, v);
+                    store8_global(static_cast<float*>(args.out) + at, v);
                 else
                     store8(static_cast<__nv_bfloat16*>(args.out) + at, v);
             };

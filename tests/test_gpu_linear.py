@@ -213,6 +213,26 @@ def test_checkpoint_blocks_with_infinities_and_nans_come_back_as_such():
     assert bool(out[3].isfinite().all())
 
 
+@pytest.mark.parametrize("skip", [4, 8])  # floats: a start on a 16- and on a 32-byte boundary
+def test_fp32_buffers_on_any_16_byte_boundary(skip):
+    rows, N, K = 37, 264, 72
+    g = torch.Generator(device="cuda").manual_seed(skip)
+    v = torch.randn(skip + rows * N, generator=g, device="cuda")[skip:].view(rows, N)
+    codes, scales = moe.alloc_checkpoint(rows, N)
+    moe.moe_checkpoint_save(v, codes, scales)
+    assert torch.equal(scales.double(), R.quantise(v)[1])
+    buf = torch.full((skip + rows * N + 8,), 3.0, device="cuda")
+    out = buf[skip:skip + rows * N].view(rows, N)
+    moe.moe_checkpoint_restore(codes, scales, out)
+    assert torch.equal(out.double(), R.values(codes, scales).float().double())
+    assert bool((buf[:skip] == 3).all()) and bool((buf[skip + rows * N:] == 3).all())
+    t = R.inputs((rows,), K, N, bf, 31)
+    buf.fill_(3)
+    moe.grouped_linear(t["x"], None, t["W"], t["bias"], act="silu", out=out)
+    check_y(out, t, (rows,), K, "silu", rows)
+    assert bool((buf[:skip] == 3).all()) and bool((buf[skip + rows * N:] == 3).all())
+
+
 @pytest.mark.parametrize("shape", SHAPES, ids=ids)
 def test_train_keeps_y_and_the_checkpoint(shape):
     counts, K, N = shape

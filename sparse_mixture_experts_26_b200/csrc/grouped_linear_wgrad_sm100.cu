@@ -450,7 +450,7 @@ cudaError_t launch_wgrad(const LinearBwdArgs& a, int width) {
 }
 
 // Average rows per group below which a bf16 gradient is bound by its epilogue.
-constexpr int kShortRows = 64;
+constexpr int kShortRows = 128;
 
 struct Layout {
     bool pair;
@@ -460,7 +460,7 @@ struct Layout {
 // The layout with the least clocks (as in grouped_linear_sm100.cu; fitted likewise) for groups of
 // the average size, the gradient's bytes to HBM being a floor for all; of layouts at the floor the
 // first wins.  Measured, zero data (us; pairs, then single SMs with 256, 128 and 64 inputs):
-//   8 groups, 256 rows, K 4096, N 14336, bf16     182  168  231  384   (sixteen epilogue warps)
+//   8 groups, 256 rows, K 4096, N 14336, bf16     181  168  257  459   (sixteen epilogue warps)
 //   8 groups, 1024 rows, K 4096, N 14336, bf16    194  201  239  371
 //   8 groups, 8192 rows, K 4096, N 14336, bf16    554  641  777 1140
 //   8 groups, 512 rows, K 4096, N 14336, fp32     338  341  317  404
@@ -484,19 +484,18 @@ Layout choose_layout(const LinearBwdArgs& a, int el) {
         const float load = 64.f * (2.f * row_z + boxes * row_x);
         const float block = fmaxf(fmaxf(2.02f * wide, 260.f + 1.1f * wide), load);
         const float products = static_cast<float>((n + 63) / 64) * block;
-        const float epilogue = el == 2 ? 1200.f + 7.3f * wide : 24.5f * wide;
+        const float epilogue =
+            el == 2 ? 1200.f + 7.3f * wide : fmaxf(850.f + 17.1f * wide, 25.f * wide);
         float clocks = static_cast<float>(rounds) * fmaxf(products, epilogue) + epilogue;
         if (pair) clocks += 6500.f;
         if (clocks < floor) clocks = floor;
         if (least == 0.f || clocks < least) best = {pair, width}, least = clocks;
     };
-    const bool pairs = n >= kShortRows && pair_gemm_enabled();
-    if (pairs && n >= 2 * kShortRows) offer(true, kN);
+    if (n >= kShortRows && pair_gemm_enabled()) offer(true, kN);
     if (el == 4) offer(false, 128);
     offer(false, kN);
     if (el == 2) offer(false, 128);
     offer(false, 64);
-    if (pairs && n < 2 * kShortRows) offer(true, kN);
     return best;
 }
 
@@ -508,10 +507,11 @@ cudaError_t launch_typed(const LinearBwdArgs& a) {
         if (err == cudaSuccess || err == cudaErrorInvalidValue) return err;
         cudaGetLastError();  // no room for a pair of CTAs: single SMs
     }
-    // Short reductions in bf16 are bound by the epilogue: sixteen warps of it (32 rows, as
-    // above: 149 us against 169 with eight and four stages).  fp32 has half the values per
-    // byte and twice the bytes, where more writers only scatter them (341 against 316 us).
-    if (!F32 && a.rows / a.E < kShortRows) return launch_wgrad<false, F32, 64, 2, 4>(a, l.width);
+    // Short reductions in bf16 are bound by the epilogue: sixteen warps of it and three stages
+    // (K 4096, N 14336, 8 groups: 256 rows 168 us against 182 with eight warps and four stages,
+    // 512 rows 175 and 187, 1024 rows 206 and 198).  fp32 has half the values per byte and twice
+    // the bytes, where more writers only scatter them (341 against 316 us).
+    if (!F32 && a.rows / a.E < kShortRows) return launch_wgrad<false, F32, 64, 3, 4>(a, l.width);
     return launch_wgrad<false, F32, 64, 4, 2>(a, l.width);
 }
 

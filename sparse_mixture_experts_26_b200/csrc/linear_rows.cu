@@ -8,7 +8,7 @@
 //
 // Bytes: dy 2, code 1.125, dz 2 per value; 25 instructions a value (GELU) weigh as much.  A
 // block takes 256 columns of a chunk of 64 to 512 rows of one group: a warp reads 512 bytes of
-// a row, eight columns a lane, and the eight warps take the rows in turn, two (or four) in
+// a row, eight columns a lane, and the eight warps take the rows in turn, two to four in
 // flight a thread.  The warps' column sums are added in order in shared memory; the chunks' go
 // to the workspace, and the block that brings a group's last chunk adds them in chunk order
 // (whichever block that is, so db does not depend on the timing).  Without an activation dz
@@ -41,10 +41,10 @@ struct DzArgs {
     float* db;             // nullptr: not wanted
     float* part;           // the chunk sums of groups with several
     uint32_t* counters;    // one for each group and strip, zero between calls
-    int items;             // chunks times strips
+    int dz_items;          // chunks times column strips of dz
+    int items;             // .. and groups times column strips of x (for the tails)
     int chunk_rows;        // a multiple of kTailRows
-    int strips;            // column strips of a chunk: the first n_strips of dz, then of x
-    int n_strips;
+    int n_strips, x_strips;
 };
 
 struct Groups {
@@ -67,6 +67,33 @@ __device__ __forceinline__ void load_groups(const DzArgs& a, Groups& g) {
     if (lane == 0) g.chunk[0] = 0;
 }
 
+// The rows of group e from its last whole block of 64 on, and how many rows of the tail buffers
+// they and the zeros behind them take.
+struct Tail {
+    int whole, rows;
+    __device__ __forceinline__ explicit Tail(int of_group) {
+        whole = of_group / kTailRows * kTailRows;
+        rows = (of_group - whole + 15) / 16 * 16;
+    }
+};
+
+// One strip of columns of the tail of group e's x.
+__device__ __forceinline__ void x_item(const DzArgs& a, const Groups& groups, int e, int strip) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = strip * kCols + lane * 8;
+    const int row0 = groups.off[e], of_group = groups.off[e + 1] - row0;
+    const Tail t(of_group);
+    if (c >= a.K) return;
+#pragma unroll 4
+    for (int r = warp; r < t.rows; r += kWarps) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (t.whole + r < of_group)
+            v = *reinterpret_cast<const uint4*>(
+                a.x + static_cast<size_t>(row0 + t.whole + r) * a.K + c);
+        *reinterpret_cast<uint4*>(a.x_tail + (static_cast<size_t>(e) * kTailRows + r) * a.K + c) = v;
+    }
+}
+
 // One chunk's strip of columns.  All threads of the block call this together.
 template <int FLIGHT>
 __device__ __forceinline__ void dz_item(const DzArgs& a, const Groups& groups,
@@ -74,7 +101,7 @@ __device__ __forceinline__ void dz_item(const DzArgs& a, const Groups& groups,
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int* off = groups.off;
     int strip;
-    const int chunk = divide(item, a.strips, strip);
+    const int chunk = divide(item, a.n_strips, strip);
     const int e = __popc(__ballot_sync(0xffffffffu, lane < a.E && groups.chunk[lane + 1] <= chunk));
     if (e == a.E) return;
     const int i = chunk - groups.chunk[e];  // chunk i of the group's
@@ -84,24 +111,12 @@ __device__ __forceinline__ void dz_item(const DzArgs& a, const Groups& groups,
     const int end = min(first + a.chunk_rows, of_group);
     const int row0 = off[e];
     // the group's last, partial block of 64 rows, if it is in this chunk
-    const int whole = of_group / kTailRows * kTailRows;
-    const bool tail = a.dz_tail != nullptr && end == of_group && whole < of_group;
-    const int end16 = whole + (of_group - whole + 15) / 16 * 16;  // zero rows up to here
+    const Tail t(of_group);
+    const bool tail = a.dz_tail != nullptr && end == of_group && t.rows > 0;
+    const int whole = t.whole, end16 = whole + t.rows;  // zero rows up to here
     const size_t trow = static_cast<size_t>(e) * kTailRows;
     const float zero[8] = {};
 
-    if (strip >= a.n_strips) {  // x's tail
-        const int c = (strip - a.n_strips) * kCols + lane * 8;
-        if (!tail || c >= a.K) return;
-#pragma unroll 4
-        for (int r = whole + warp; r < end16; r += kWarps) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (r < end)
-                v = *reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(row0 + r) * a.K + c);
-            *reinterpret_cast<uint4*>(a.x_tail + (trow + r - whole) * a.K + c) = v;
-        }
-        return;
-    }
     const int c = strip * kCols + lane * 8;
     const bool have = c < a.N && (a.codes || a.db || tail);  // else nothing to do here
     const int nb = ckpt_blocks(a.N);
@@ -200,8 +215,13 @@ __global__ void __launch_bounds__(kThreads, BLOCKS_PER_SM) linear_dz_kernel(cons
     pdl_launch_dependents();
     if (threadIdx.x < 32) load_groups(a, groups);
     __syncthreads();
-    for (int item = blockIdx.x; item < a.items; item += gridDim.x)
-        dz_item<FLIGHT>(a, groups, s_sum, s_last, item);
+    int item = blockIdx.x;
+    for (; item < a.dz_items; item += gridDim.x) dz_item<FLIGHT>(a, groups, s_sum, s_last, item);
+    for (; item < a.items; item += gridDim.x) {
+        int strip;
+        const int e = divide(item - a.dz_items, a.x_strips, strip);
+        x_item(a, groups, e, strip);
+    }
 }
 
 }  // namespace
@@ -226,7 +246,7 @@ cudaError_t launch_linear_dz(const LinearBwdArgs& a) {
     d.part = a.db_part;
     d.counters = a.db_counters;
     d.n_strips = (a.N + kCols - 1) / kCols;
-    d.strips = d.n_strips + (a.dW ? (a.K + kCols - 1) / kCols : 0);
+    d.x_strips = a.dW ? (a.K + kCols - 1) / kCols : 0;
     // Blocks stay for several items, because reading the group bounds takes a block as long
     // as one; and chunks grow while there are several items for every block.  Where the
     // counters are too few, a group is one chunk: its strips (more than 256) are work enough.
@@ -238,14 +258,22 @@ cudaError_t launch_linear_dz(const LinearBwdArgs& a) {
     } else {
         for (d.chunk_rows = kTailRows;; d.chunk_rows *= 2) {
             chunks = a.rows / d.chunk_rows + a.E;  // at most linear_chunks
-            if (d.chunk_rows >= 512 || chunks * d.strips < 6LL * blocks) break;
+            if (d.chunk_rows >= 512 || chunks * d.n_strips < 6LL * blocks) break;
         }
     }
-    d.items = static_cast<int>(chunks * d.strips);  // rows * N, rows * K < 2^40: below 2^31
-    // Few items are chains of latencies: four rows in flight where two blocks an SM hold them all
-    // (164 x 176 6.9 -> 6.1 us, 1616 x 824 7.8 -> 7.2; but 8192 x 14336 134 -> 155).
-    if (d.items <= 2 * device_sm_count())
+    d.dz_items = static_cast<int>(chunks * d.n_strips);  // rows * N < 2^40: below 2^31
+    d.items = d.dz_items + a.E * d.x_strips;
+    // Few items are chains of latencies: more rows in flight where two or three blocks an SM hold
+    // them all (counting half a chunk for a group's last, partial one).  Us with 2 rows and four
+    // blocks, 3 and three, 4 and two: 1958 x 1168, 16 groups (GELU) 9.1, 8.9, 8.6; 600 x 7168, 8
+    // groups (SiLU) 12.0, 10.0, 11.7; 2048 x 4096 (SiLU) 12.5, 14.3, 14.7.
+    const int sms = device_sm_count();
+    if (d.items <= 2 * sms)
         return launch_k(linear_dz_kernel<4, 2>, d.items, kThreads, 0, a.stream, d);
+    const long long full = (chunks - a.E + (a.E + 1) / 2) * d.n_strips + a.E * d.x_strips / 2;
+    if (full <= 3LL * sms)
+        return launch_k(linear_dz_kernel<3, 3>, d.items < 3 * sms ? d.items : 3 * sms, kThreads, 0,
+                        a.stream, d);
     return launch_k(linear_dz_kernel<2, kBlocksPerSm>, d.items < blocks ? d.items : blocks, kThreads, 0, a.stream, d);
 }
 

@@ -32,8 +32,10 @@
 // anybody.  Pairs do not share: they run at the power limit, where an idle SM lets the others
 // clock higher (4096 x 14336 x 4096: 1286 TFLOP/s unshared, 1232 shared).
 //
-// Measured: 4096^3 1400 TFLOP/s, 8192 x 4096 x 14336 1263 to 1372 (cuBLAS 1493 and 1310);
-// 8 experts, 32 rows, 14336 -> 4096 in 134 to 144 us, 98 to 106 % of a copy's bandwidth.
+// Measured, rows x K x N in TFLOP/s after a pause (cuBLAS in parentheses): 4096^3 1440 (1500),
+// 4096 x 14336 x 4096 1419 (1527), 8192 x 4096 x 14336 1569 (1527), 4096 x 2048 x 7168 1403
+// (1325), 8192 x 512 x 7168 956 (938); without pauses the power limit takes a fifth.  8 experts,
+// 32 rows, 14336 -> 4096: 134 to 143 us, 98 to 106 % of a copy's bandwidth.
 //
 // Every wait is bounded (sm100_ptx.cuh).
 #include <cuda.h>

@@ -335,14 +335,16 @@ moe_status moe_grouped_linear(const void *x, const int32_t *offsets, const void 
  *   scale s = max|v| / 128, code q = floor(v / s) in [-128, 127], and q stands for
  *   (q + 1/2) s:  codes [rows, N] int8, scales [rows, ceil(N / 32)] float.
  * The value is off by at most s / 2 = max|v| / 256, and its sign is kept (v >= 0 gives
- * q >= 0), so that a ReLU's mask survives.  A block whose largest magnitude is below
+ * q >= 0, v < 0 gives q < 0).  Zero itself has no code: beside other values it comes back as
+ * s / 2, so values of which many are zero (a ReLU's output) gain an offset.  A block whose largest magnitude is below
  * 2^-100 is kept as zeros (s = 0); one that holds an infinity or NaN comes back as
  * infinities or NaN. */
 #define MOE_CHECKPOINT_BLOCK 32
 
 /* moe_grouped_linear for training: the same y, and the pre-activations z kept as an
  * 8-bit checkpoint (codes, scales) for moe_grouped_linear_backward: 1.125 bytes a
- * value.  z is taken from the fp32 accumulator; where z / s is less than about 2^-15 above a
+ * value.  With MOE_ACT_RELU a z of exactly zero takes the code below zero (-s / 2), so that
+ * q >= 0 where z > 0 and nowhere else: the backward's mask is the forward's.  z is taken from the fp32 accumulator; where z / s is less than about 2^-15 above a
  * whole number, the code may be the one below.  dt must be MOE_BF16
  * (MOE_ERR_UNSUPPORTED otherwise). */
 moe_status moe_grouped_linear_train(const void *x, const int32_t *offsets, const void *W,

@@ -594,7 +594,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (args.codes != nullptr) {
                     const float s = ckpt_scale(ckpt_amax_block(have_f ? ckpt_amax8(v) : 0.f));
                     if (valid) {
-                        *reinterpret_cast<uint2*>(args.codes + at) = ckpt_pack8_sums(v, s);
+                        // a ReLU's slope at zero is zero: the backward tells z > 0 by the code
+                        *reinterpret_cast<uint2*>(args.codes + at) =
+                            args.act == MOE_ACT_RELU ? ckpt_pack8_sums<true>(v, s)
+                                                     : ckpt_pack8_sums<false>(v, s);
                         if ((lane & 3) == 0)
                             args.scales[static_cast<size_t>(t.row0 + tok) * nb + f / kCkptBlock] =
                                 s;

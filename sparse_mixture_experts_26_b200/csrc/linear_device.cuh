@@ -231,11 +231,16 @@ __device__ __forceinline__ uint2 ckpt_pack8_bf16(const float (&v)[8], float s) {
 // without a clamp.  A value within 2^-15 of a step may take the code below it; the sign is
 // kept.  (15 instructions a value the exact way, 2 this way: training's epilogue at K = 2048
 // is bound by them.)
+// BELOW_ZERO: a zero takes the code below it, so that q >= 0 says z > 0: rounded up from one less
+// instead of down, which differs only at whole products (others' codes are short of theirs anyway).
+template <bool BELOW_ZERO>
 __device__ __forceinline__ uint2 ckpt_pack8_sums(const float (&v)[8], float s) {
     const float inv = ckpt_inverse(s) * (1.0f - 0x1p-22f);
     uint32_t c[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = __float_as_uint(__fmaf_rd(v[i], inv, 12582912.f));
+    for (int i = 0; i < 8; ++i)
+        c[i] = __float_as_uint(BELOW_ZERO ? __fmaf_ru(v[i], inv, 12582911.f)
+                                          : __fmaf_rd(v[i], inv, 12582912.f));
     return ckpt_bytes8(c);
 }
 // (q + 1/2) s = q s + s/2 in one rounding.  A byte with its sign bit flipped is q + 128;

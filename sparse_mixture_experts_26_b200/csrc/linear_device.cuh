@@ -86,10 +86,15 @@ __device__ __forceinline__ void sigmoids(float z0, float z1, float& s0, float& s
     s1 = r * d0;
 }
 
+// SiLU z / (1 + e^-z), relative to itself as far down as e^z is a normal number, zero below; one
+// reciprocal a value, so that nothing has to be held inside fp32 and a NaN stays with its own.
+__device__ __forceinline__ float silu(float z) {
+    return max_nan(z, -200.f) * rcp_approx(1.0f + ex2_approx(-1.44269504f * z));
+}
+
 // v = act(v), also far out: a NaN stays one (and leaves its neighbour alone), infinities give
 // the limits.
 //   GELU: z Phi(z) = max(z, 0) - |z| Phi(-|z|), |z| at most 24, where Phi is zero
-//   SiLU: z at least -43, as in sigmoids()
 __device__ __forceinline__ void act_value8(int act, float (&v)[8]) {
     if (act == MOE_ACT_GELU) {
 #pragma unroll
@@ -103,12 +108,7 @@ __device__ __forceinline__ void act_value8(int act, float (&v)[8]) {
         }
     } else if (act == MOE_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            float s0, s1;
-            sigmoids(v[i], v[i + 1], s0, s1);
-            v[i] = max_nan(v[i], -43.f) * s0;
-            v[i + 1] = max_nan(v[i + 1], -43.f) * s1;
-        }
+        for (int i = 0; i < 8; ++i) v[i] = silu(v[i]);
     } else if (act == MOE_ACT_RELU) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = v[i] <= 0.f ? 0.f : v[i];

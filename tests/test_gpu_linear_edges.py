@@ -47,3 +47,26 @@ def test_relu_gradient_of_exact_zeros(counts, K, N):
     assert torch.equal(db.double(), rb)
     assert torch.equal(dx, rx.to(bf)) and torch.equal(dW, rW.to(bf))
     assert not bool(dW[:, ::3].any())
+
+
+FAR_SILU = [-float("inf"), -1e30, -2.0 ** 44, -200.0, -104.0, -95.0, -86.5, -70.0, -60.0, -50.0,
+            -44.0, -43.5, -43.0, -42.0, -30.0, -17.0, -3.0, -0.5, 0.0, 0.5, 17.0, 30.0, 43.0, 60.0,
+            200.0, 1e30]
+
+
+@pytest.mark.parametrize("dtype,y_dtype", [(bf, bf), (bf, f32), (f32, f32)])
+def test_silu_far_below_zero(dtype, y_dtype):
+    """z e^z, which goes to 0, relative to itself while e^z is a normal number.  Its argument is
+    rounded twice: |z| log2 e 2^-23 ln 2 <= 87 2^-23 < 2^-16; the rest is a few roundings."""
+    z = torch.tensor(FAR_SILU, dtype=torch.float64, device="cuda")
+    z = torch.cat([z, z.flip(0), z.roll(7)])[:72].to(dtype)  # three neighbourhoods
+    x = torch.zeros(3, 16, dtype=dtype, device="cuda")
+    W = torch.ones(1, 72, 16, dtype=dtype, device="cuda")
+    y = torch.empty(3, 72, dtype=y_dtype, device="cuda")
+    moe.grouped_linear(x, None, W, z[None], act="silu", out=y)
+    zd = z.double()
+    ref = torch.where(zd < 0, zd.clamp(min=-800) * torch.exp(zd.clamp(min=-800)) /
+                      (1 + torch.exp(zd)), zd / (1 + torch.exp(-zd)))
+    tol = (2.0 ** -15 + (R.U_BF16 if y_dtype == bf else 0)) * ref.abs() + 1e-35
+    err = (y.double() - ref).abs()
+    assert bool((err <= tol).all()), (err / tol).max()

@@ -22,10 +22,15 @@ __device__ __forceinline__ float ex2_approx(float v) {
     return r;
 }
 
-// The larger one, or NaN if either is.
+// The larger one, the smaller one, or NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
 
@@ -76,16 +81,6 @@ __device__ __forceinline__ F2 normal_tails(float x0, float x1, F2& e) {
     p = f2_fma(p, t, f2_all(0.127414796f));
     return f2_mul(f2_mul(p, t), e);
 }
-// 1 / (1 + e^-z) of two z, with one reciprocal; z counts as -43 below that (2e-19), where
-// the product of the two denominators would leave fp32.
-__device__ __forceinline__ void sigmoids(float z0, float z1, float& s0, float& s1) {
-    const float d0 = 1.0f + ex2_approx(-1.44269504f * fmaxf(z0, -43.f));
-    const float d1 = 1.0f + ex2_approx(-1.44269504f * fmaxf(z1, -43.f));
-    const float r = rcp_approx(d0 * d1);
-    s0 = r * d1;
-    s1 = r * d0;
-}
-
 // SiLU z / (1 + e^-z), relative to itself as far down as e^z is a normal number, zero below; one
 // reciprocal a value, so that nothing has to be held inside fp32 and a NaN stays with its own.
 __device__ __forceinline__ float silu(float z) {
@@ -117,7 +112,8 @@ __device__ __forceinline__ void act_value8(int act, float (&v)[8]) {
 
 // g *= act'(z); the slope of ReLU at 0 is 0.
 //   GELU: Phi(z) + z phi(z), phi the normal density
-//   SiLU: s (1 + z (1 - s)), s = 1 / (1 + e^-z)
+//   SiLU: s (1 + z (1 - s)), s = 1 / (1 + e^-z), where z (1 - s) is taken as z e^-z s for z > 0,
+//   so that it vanishes for large z
 __device__ __forceinline__ void act_slope8(int act, const float (&z)[8], float (&g)[8]) {
     if (act == MOE_ACT_GELU) {
 #pragma unroll
@@ -134,12 +130,10 @@ __device__ __forceinline__ void act_slope8(int act, const float (&z)[8], float (
         }
     } else if (act == MOE_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            float s[2];
-            sigmoids(z[i], z[i + 1], s[0], s[1]);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                g[i + k] *= s[k] * fmaf(max_nan(z[i + k], -43.f), 1.0f - s[k], 1.0f);
+        for (int i = 0; i < 8; ++i) {
+            const float e = ex2_approx(-1.44269504f * z[i]), s = rcp_approx(1.0f + e);
+            const float rest = z[i] > 0.f ? e * s : 1.0f - s;
+            g[i] *= s * fmaf(max_nan(min_nan(z[i], 200.f), -200.f), rest, 1.0f);
         }
     } else if (act == MOE_ACT_RELU) {
 #pragma unroll

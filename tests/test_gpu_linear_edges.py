@@ -70,3 +70,44 @@ def test_silu_far_below_zero(dtype, y_dtype):
     tol = (2.0 ** -15 + (R.U_BF16 if y_dtype == bf else 0)) * ref.abs() + 1e-35
     err = (y.double() - ref).abs()
     assert bool((err <= tol).all()), (err / tol).max()
+
+
+# -------------------------------------------------------------------- slopes, value by value
+def slopes_of(z, name):
+    """The kernel's slope at every z [N] (each (q + 1/2) s of one of the blocks' scales)."""
+    codes, scales, N = z["codes"], z["scales"], z["codes"].shape[1]
+    rows = codes.shape[0]
+    db = torch.empty(rows, N, device="cuda")  # a group a row: db is dz itself, in fp32
+    off = torch.arange(rows + 1, dtype=torch.int32, device="cuda")
+    x = torch.zeros(rows, 8, dtype=bf, device="cuda")
+    W = torch.zeros(rows, N, 8, dtype=bf, device="cuda")
+    ws = moe.alloc_grouped_linear_backward_workspace(rows, 8, N, rows)
+    moe.moe_grouped_linear_backward(torch.ones(rows, N, dtype=bf, device="cuda"), x, off, W, ws,
+                                    db=db, codes=codes, scales=scales, act=name)
+    return db.double()
+
+
+def every_code(scales):
+    """Rows of all 256 codes, in blocks whose neighbours differ; one scale (exact) a row."""
+    q = (torch.arange(256, device="cuda").view(2, 128).t().reshape(1, -1) - 128).to(torch.int8)
+    codes = q.repeat(len(scales), 1).contiguous()
+    s = torch.tensor(scales, device="cuda")[:, None].repeat(1, 8).contiguous()
+    return dict(codes=codes, scales=s, z=R.values(codes, s))
+
+
+@pytest.mark.parametrize("scale", [0.25, 2.0, 4.0, 8.0, 2.0 ** 10])
+def test_silu_slope_beside_far_neighbours(scale):
+    """s (1 + z (1 - s)) for every code of a block, whatever stands beside it: 1 for large z.  The
+    exponential's argument is rounded twice: |z| log2 e 2^-23 ln 2 <= |z| 2^-23; the rest is a few
+    roundings, times the condition of 1 + z (1 - s), at most 8 away from its zero near -1.28."""
+    t = every_code([scale])
+    z = t["z"]
+    got = slopes_of(t, "silu")
+    e = torch.exp(-z.abs())  # without the loss of 1 - s in 64 bits
+    s, c = torch.where(z > 0, 1.0, e) / (1 + e), torch.where(z > 0, e, 1.0) / (1 + e)
+    want = s * (1 + z * c)
+    live = z >= -85  # beyond, e^z leaves the normal numbers
+    err = (got - want).abs()
+    tol = (z.abs().clamp(max=85) + 8) * 2.0 ** -22 * (s * (1 + z.abs() * c))
+    assert bool((err <= tol)[live].all()), float((err / tol)[live].max())
+    assert bool((err <= 1e-34)[~live].all())

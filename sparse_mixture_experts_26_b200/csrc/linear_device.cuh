@@ -111,22 +111,22 @@ __device__ __forceinline__ void act_value8(int act, float (&v)[8]) {
 }
 
 // g *= act'(z); the slope of ReLU at 0 is 0.
-//   GELU: Phi(z) + z phi(z), phi the normal density
+//   GELU: Phi(z) + z phi(z), phi the normal density: with x = |z| and d = x phi(x) - Phi(-x),
+//   1 + d, or -d for z < 0, where Phi(-x) is all there is and keeps its bits
 //   SiLU: s (1 + z (1 - s)), s = 1 / (1 + e^-z), where z (1 - s) is taken as z e^-z s for z > 0,
 //   so that it vanishes for large z
 __device__ __forceinline__ void act_slope8(int act, const float (&z)[8], float (&g)[8]) {
     if (act == MOE_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            F2 e2;
-            float t[2], e[2];
-            f2_get(normal_tails(fminf(fabsf(z[i]), 24.f), fminf(fabsf(z[i + 1]), 24.f), e2), t[0],
-                   t[1]);
-            f2_get(e2, e[0], e[1]);
+            F2 e;
+            const float x0 = min_nan(fabsf(z[i]), 24.f), x1 = min_nan(fabsf(z[i + 1]), 24.f);
+            const F2 t = normal_tails(x0, x1, e);
+            float d[2];
+            f2_get(f2_fma(f2_mul(f2(x0, x1), f2_all(0.39894228f)), e, f2_mul(t, f2_all(-1.0f))),
+                   d[0], d[1]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                g[i + k] *= fmaf(0.39894228f * z[i + k], e[k], 0.5f) +
-                            copysignf(0.5f - t[k], z[i + k]);
+            for (int k = 0; k < 2; ++k) g[i + k] *= z[i + k] < 0.f ? -d[k] : 1.0f + d[k];
         }
     } else if (act == MOE_ACT_SILU) {
 #pragma unroll

@@ -111,3 +111,25 @@ def test_silu_slope_beside_far_neighbours(scale):
     tol = (z.abs().clamp(max=85) + 8) * 2.0 ** -22 * (s * (1 + z.abs() * c))
     assert bool((err <= tol)[live].all()), float((err / tol)[live].max())
     assert bool((err <= 1e-34)[~live].all())
+
+
+def test_gelu_slope_in_its_tail():
+    """z Phi'(z) + Phi(z) for z in [-6, -2], relative to itself.  Phi(-x) comes from Abramowitz and
+    Stegun 7.1.26, whose own error is taken from the formula in 64 bits.  The rest is rounding:
+    exp(-x^2 / 2) has its argument (up to 26 in log2) rounded twice and two constants by 2^-25, so
+    26 (2^-23 + 2^-24) ln 2 < 2^-18; exp2's 2^-22 and five roundings of 2^-24; the sum of the two
+    terms has a condition of at most 1.6 here: less than 2^-16 in all."""
+    t = every_code([3 / 64, 1 / 32])
+    z = t["z"]
+    x = z.abs()
+    got = slopes_of(t, "gelu")
+    tail = 0.5 * torch.erfc(x / math.sqrt(2))
+    u = 1 / (1 + 0.3275911 / math.sqrt(2) * x)
+    poly = ((((1.061405429 * u - 1.453152027) * u + 1.421413741) * u - 0.284496736) * u
+            + 0.254829592) * u
+    published = 0.5 * poly * torch.exp(-x * x / 2)
+    want = tail + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)  # z < 0
+    at = (z >= -6) & (z <= -2)
+    assert int(at.sum()) > 100
+    tol = (published - tail).abs() + 2.0 ** -16 * want.abs()
+    assert bool(((got - want).abs() <= tol)[at].all()), float(((got - want).abs() / tol)[at].max())

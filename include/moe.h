@@ -323,8 +323,10 @@ size_t moe_grouped_linear_workspace_bytes(int rows, int K, int N, int E, moe_dty
  *   residual [rows, N]  dt in, or NULL; may be y itself when y_dt == dt
  *   y        [rows, N]  y_dt out
  * dt == MOE_BF16: tensor cores with fp32 accumulation, everything up to y in fp32 and
- * one rounding to y_dt (MOE_BF16, or MOE_F32 as moe_combine reads it).  dt == MOE_F32:
- * fp32 throughout on CUDA cores, y_dt == MOE_F32. */
+ * one rounding to y_dt (MOE_BF16, or MOE_F32 as moe_combine reads it); the GELU there is
+ * made for a bf16 output, off by about 1e-7 |z| (4e-3 of itself at z = -6).  dt == MOE_F32:
+ * fp32 throughout on CUDA cores, the activations within 6 units in the last place, y_dt ==
+ * MOE_F32. */
 moe_status moe_grouped_linear(const void *x, const int32_t *offsets, const void *W,
                               const void *bias, const void *residual, int rows, int K, int N,
                               int E, moe_act act, moe_dtype dt, moe_dtype y_dt, void *y, void *ws,
@@ -359,7 +361,7 @@ moe_status moe_checkpoint_save(const void *v, int rows, int N, moe_dtype dt, int
 
 /* out [rows, N] (out_dt) = act(value of each code), rounded once: with MOE_ACT_NONE the
  * kept values themselves, else for example the next projection's input recomputed from
- * this one's checkpoint. */
+ * this one's checkpoint (GELU as in moe_grouped_linear with MOE_BF16). */
 moe_status moe_checkpoint_restore(const int8_t *codes, const float *scales, int rows, int N,
                                   moe_act act, moe_dtype out_dt, void *out, cudaStream_t stream);
 

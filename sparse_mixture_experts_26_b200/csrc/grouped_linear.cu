@@ -35,6 +35,18 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool have) 
                  : "memory");
 }
 
+// act(z) in fp32, relative to itself: the approximations of act_value8 (1e-7 absolute) are made
+// for epilogues that round to bf16.  Here the products take longer than CUDA's functions.
+// Infinities give the limits (Phi(-16) is zero, and e^-200).
+__device__ __forceinline__ float act_f32(int act, float z) {
+    if (act == MOE_ACT_GELU) return max_nan(z, -16.f) * normcdff(z);
+    if (act == MOE_ACT_SILU) {
+        const float t = expf(-fabsf(z));
+        return __fdividef(max_nan(z, -200.f) * (z < 0.f ? t : 1.0f), 1.0f + t);
+    }
+    return act == MOE_ACT_RELU && z <= 0.f ? 0.f : z;
+}
+
 template <int RM, int RN>
 __global__ void __launch_bounds__(kThreads) linear_f32_kernel(const LinearArgs a, int ftiles) {
     using Tile = F32Tile<RM, RN>;
@@ -130,7 +142,8 @@ __global__ void __launch_bounds__(kThreads) linear_f32_kernel(const LinearArgs a
             v[k] = acc[i + k / RN][k % RN] +
                    (bias && f < a.N ? bias[static_cast<size_t>(e) * a.N + f] : 0.f);
         }
-        act_value8(a.act, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = act_f32(a.act, v[k]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int f = f0 + tx + 8 * (k % RN), r = row0 + ty + 16 * (i + k / RN);

@@ -133,3 +133,17 @@ def test_gelu_slope_in_its_tail():
     assert int(at.sum()) > 100
     tol = (published - tail).abs() + 2.0 ** -16 * want.abs()
     assert bool(((got - want).abs() <= tol)[at].all()), float(((got - want).abs() / tol)[at].max())
+
+
+@pytest.mark.parametrize("name", ["gelu", "silu"])
+def test_fp32_activations_relative_to_themselves(name):
+    """The fp32 operator is fp32 throughout: normcdff is within 5 units in the last place and one
+    rounding follows; expf is within 2, and so is the quotient, with a sum and a product."""
+    z = torch.linspace(-12, 12, 4096, dtype=torch.float64).float().cuda()
+    x, W = torch.zeros(2, 8, device="cuda"), torch.ones(1, 4096, 8, device="cuda")
+    y = moe.grouped_linear(x, None, W, z[None], act=name).double()
+    zd = z.double()
+    ref = (zd * 0.5 * torch.erfc(-zd / math.sqrt(2)) if name == "gelu"
+           else zd / (1 + torch.exp(-zd)))
+    assert bool(((y - ref).abs() <= 6 * 2.0 ** -23 * ref.abs()).all()), float(
+        ((y - ref).abs() / ref.abs()).nan_to_num().max())

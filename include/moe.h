@@ -346,9 +346,10 @@ moe_status moe_grouped_linear(const void *x, const int32_t *offsets, const void 
 /* moe_grouped_linear for training: the same y, and the pre-activations z kept as an
  * 8-bit checkpoint (codes, scales) for moe_grouped_linear_backward: 1.125 bytes a
  * value.  With MOE_ACT_RELU a z of exactly zero takes the code below zero (-s / 2), so that
- * q >= 0 where z > 0 and nowhere else: the backward's mask is the forward's.  z is taken from the fp32 accumulator; where z / s is less than about 2^-15 above a
- * whole number, the code may be the one below.  dt must be MOE_BF16
- * (MOE_ERR_UNSUPPORTED otherwise). */
+ * q >= 0 where z > 0 and nowhere else: the backward's mask is the forward's.  z is taken
+ * from the fp32 accumulator; where |z / s| is a whole number or less than 2^-14 above one,
+ * the code may be the neighbour nearer zero, and the value off by (1/2 + 2^-14) s.  dt must
+ * be MOE_BF16 (MOE_ERR_UNSUPPORTED otherwise). */
 moe_status moe_grouped_linear_train(const void *x, const int32_t *offsets, const void *W,
                                     const void *bias, const void *residual, int rows, int K,
                                     int N, int E, moe_act act, moe_dtype dt, moe_dtype y_dt,

@@ -222,9 +222,10 @@ __device__ __forceinline__ uint2 ckpt_pack8_bf16(const float (&v)[8], float s) {
 }
 // The same for fp32 sums, whose last bits are rounding anyway: one multiply-add that rounds
 // down is the floor, and a reciprocal short of 1 / s by about 2^-22 keeps |v / s| below 128
-// without a clamp.  A value within 2^-15 of a step may take the code below it; the sign is
-// kept.  (15 instructions a value the exact way, 2 this way: training's epilogue at K = 2048
-// is bound by them.)
+// without a clamp.  Of a value on a step or less than 2^-14 beyond it, seen from zero, the code
+// may be the neighbour nearer zero, and the value off by (1/2 + 2^-14) s; the sign is kept.
+// (15 instructions a value the exact way, 2 this way: training's epilogue at K = 2048 is bound
+// by them.)
 // BELOW_ZERO: a zero takes the code below it, so that q >= 0 says z > 0: rounded up from one less
 // instead of down, which differs only at whole products (others' codes are short of theirs anyway).
 template <bool BELOW_ZERO>

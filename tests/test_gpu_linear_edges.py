@@ -147,3 +147,52 @@ def test_fp32_activations_relative_to_themselves(name):
            else zd / (1 + torch.exp(-zd)))
     assert bool(((y - ref).abs() <= 6 * 2.0 ** -23 * ref.abs()).all()), float(
         ((y - ref).abs() / ref.abs()).nan_to_num().max())
+
+
+# --------------------------------------------------------------------- training's codes
+@pytest.mark.parametrize("name", ["none", "relu"])
+@pytest.mark.parametrize("top", [128.0, 100.0, 255.0, 2.0 ** -90 * 3])
+def test_training_codes_around_every_step(top, name):
+    """z on each step and one unit in the last place to either side, both signs: the code is the
+    exact floor, or within 2^-14 of a step the neighbour nearer zero.  (The reciprocal is short of
+    1 / s by 2^-22 and off by 2^-23 and a rounding, and |z / s| <= 128: less than 2^-14.)  Zero has
+    the code 0, under a ReLU -1."""
+    steps = torch.arange(-127, 128, dtype=torch.float64, device="cuda") * (top / 128)
+    near = steps.float()
+    inf = torch.full_like(near, float("inf"))
+    up, down = torch.nextafter(near, inf), torch.nextafter(near, -inf)
+    up[127], down[127] = top * 2.0 ** -40, -top * 2.0 ** -40  # beside the step at 0
+    z = torch.cat([near, up, down])
+    z = torch.nn.functional.pad(z, (0, -len(z) % 31)).view(-1, 31)
+    z = torch.cat([torch.full((len(z), 1), top, device="cuda"), z], 1)  # 32 a block
+    N = z.numel()
+    # z = x W^T + b exactly, from three bf16 parts of its 24 bits
+    parts, rest = [], z.flatten()
+    for _ in range(3):
+        parts.append(rest.to(bf))
+        rest = rest - parts[-1].float()
+    assert not bool(rest.any())
+    W = torch.zeros(1, N, 8, dtype=bf, device="cuda")
+    W[0, :, :2] = torch.stack(parts[:2], 1)
+    x = torch.zeros(2, 8, dtype=bf, device="cuda")
+    x[:, :2] = 1
+    ws = moe.alloc_grouped_linear_workspace(2, 8, N, 1)
+    y = torch.empty(2, N, device="cuda")
+    codes, scales = moe.alloc_checkpoint(2, N)
+    moe.moe_grouped_linear_train(x, None, W, y, codes, scales, ws, bias=parts[2][None],
+                                 act=name)
+    out = R.act(z.flatten(), name)
+    assert torch.equal(y[0], out) and torch.equal(y[1], out)
+    v = z.flatten().double() / (top / 128)
+    assert bool((scales == top / 128).all())
+    floor = v.floor().clamp(-128, 127)
+    if name == "relu":
+        floor[v == 0] = -1
+    for got in codes.double():
+        off = got != floor
+        nearer = torch.where(v > 0, floor - 1, floor + 1)
+        assert bool((got == nearer)[off].all())
+        assert bool(((v - v.round()).abs() < 2.0 ** -14)[off].all())
+        kept = (got + 0.5 - v).abs()
+        assert bool((kept <= 0.5 + 2.0 ** -14).all())
+        assert bool(((got >= 0) == (v >= 0))[v != 0].all())

@@ -534,8 +534,11 @@ def _check_checkpoint(codes, scales, rows: int, N: int) -> None:
         _expect("scales", scales, (rows, nb), torch.float32)
 
 
-_get_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The current device and stream as bare numbers; where torch lacks these internals (a build
+# without CUDA, another release), by its public functions, a microsecond or two slower.
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _call(f, tensors, stream, *args) -> None:

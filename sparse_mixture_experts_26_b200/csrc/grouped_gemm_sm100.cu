@@ -42,7 +42,6 @@
 #include <cuda_bf16.h>
 
 #include <cstdio>
-#include <mutex>
 
 #include "moe_internal.h"
 #include "sm100_ptx.cuh"
@@ -488,27 +487,29 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// cuTensorMapEncodeTiled is a driver call: it needs a context bound to the calling thread,
-// which a thread without a runtime call of its own yet does not have.
-static void bind_thread_to_device() {
-    static thread_local bool bound = false;
-    if (bound) return;
+template <typename Fn>
+static Fn driver_entry(const char* name) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool found = cudaGetDriverEntryPoint(name, &p, cudaEnableDefault, &q) == cudaSuccess &&
+                       q == cudaDriverEntryPointSuccess;
+    return found ? reinterpret_cast<Fn>(p) : nullptr;
+}
+
+// cuTensorMapEncodeTiled is a driver call: it needs a context bound to the calling thread, which a
+// thread without a runtime call of its own yet does not have.  A thread that has one, which need
+// not be the device's primary context, keeps it.
+static void bind_thread_without_context() {
+    static const auto get_current = driver_entry<CUresult (*)(CUcontext*)>("cuCtxGetCurrent");
+    CUcontext context = nullptr;
+    if (get_current && get_current(&context) == CUDA_SUCCESS && context) return;
     int dev = 0;
-    bound = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaSetDevice(dev);
 }
 
 static EncodeTiledFn get_encode_fn() {
-    bind_thread_to_device();
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
+    bind_thread_without_context();
+    static const EncodeTiledFn fn = driver_entry<EncodeTiledFn>("cuTensorMapEncodeTiled");
     return fn;
 }
 

@@ -299,7 +299,8 @@ moe_status moe_layer_backward_events(const void *x, const void *Wg, const void *
  * -- infinities and NaN included -- reaches no result.
  * Buffers are contiguous, 16-byte aligned (offsets and the workspace too) and overlap
  * only where stated.
- * Shapes: K and N multiples of 8, 1 <= E <= 32, any rows >= 0 (rows == 0 queues
+ * Shapes: K and N multiples of 8 up to 2^30, 1 <= E <= 32, E K and E N below 2^31, rows up to
+ * 2^30 with rows K and rows N below 2^40; MOE_ERR_UNSUPPORTED beyond (rows == 0 queues
  * nothing, except that moe_grouped_linear_backward writes zero dW and db). */
 typedef enum {
     MOE_ACT_NONE = 0,

@@ -12,11 +12,13 @@ namespace moe {
 namespace {
 
 constexpr int kMaxLinearRows = 1 << 30;
+constexpr int kMaxLinearDim = 1 << 30;  // of K and N: sizes are rounded up to tiles in 32 bits
 
 moe_status check_linear(int rows, int K, int N, int E, moe_dtype dt) {
     if (rows < 0 || K <= 0 || N <= 0 || E <= 0) return MOE_ERR_INVALID_ARG;
     if (dt != MOE_F32 && dt != MOE_BF16) return MOE_ERR_INVALID_ARG;
-    if (E > kMaxExperts || K % 8 != 0 || N % 8 != 0 || rows > kMaxLinearRows)
+    if (E > kMaxExperts || K % 8 != 0 || N % 8 != 0 || rows > kMaxLinearRows ||
+        K > kMaxLinearDim || N > kMaxLinearDim)
         return MOE_ERR_UNSUPPORTED;
     // 32-bit coordinates inside one expert's weights and one array of rows; element
     // offsets are 64-bit

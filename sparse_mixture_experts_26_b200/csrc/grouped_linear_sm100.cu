@@ -571,8 +571,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // A warp that gives up leaves alone; only shares, which come before all whole
             // tiles, have barriers among the warps, and there they leave together.
-            bool ok = __all_sync(0xffffffffu, mbar_wait_asleep(&bk.tmem_full[acc], acc_phase,
-                                                               abort_flag, args.status));
+            bool ok = __all_sync(0xffffffffu,
+                                 mbar_wait_asleep(&bk.tmem_full[acc], acc_phase, abort_flag,
+                                                  args.status, reduction_limit_ns(kb1 - kb0)));
             const bool whole = kb1 - kb0 == num_kb;
             if (i < plan.pieces) ok = bar_all(ok, kVoteBarrier, kEpiThreads);
             if (!ok) break;

@@ -308,8 +308,9 @@ __global__ void __launch_bounds__(Shape<PAIR, ROWS, STAGES, GROUPS>::kThreads, 1
         for (int tile = first; tile < total; tile += step) {
             tile_of(tile, e, m0, n0, row0, n);
             if (n > 0) {
-                if (!__all_sync(0xffffffffu, mbar_wait_asleep(&bk.tmem_full[acc], acc_phase,
-                                                              abort_flag, args.status)))
+                if (!__all_sync(0xffffffffu,
+                                mbar_wait_asleep(&bk.tmem_full[acc], acc_phase, abort_flag,
+                                                 args.status, reduction_limit_ns(n / kBlock + 1))))
                     break;  // a warp that gives up leaves alone
                 tc_fence_after();
             }

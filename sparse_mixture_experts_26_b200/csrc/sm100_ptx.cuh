@@ -100,7 +100,8 @@ __device__ __forceinline__ bool elect_one() {
 // the 1000 W limit a tensor-bound kernel runs 6-9% faster this way (grouped linear, 8192 x
 // 4096 x 14336, one group: 1204 -> 1303 TFLOP/s).
 __device__ __forceinline__ bool mbar_wait_asleep(uint64_t* bar, uint32_t parity,
-                                                 volatile int* abort_flag, uint32_t* status) {
+                                                 volatile int* abort_flag, uint32_t* status,
+                                                 unsigned long long limit_ns = kWaitTimeoutNs) {
     auto try_wait = [&]() {
         uint32_t done;
         asm volatile(
@@ -116,13 +117,20 @@ __device__ __forceinline__ bool mbar_wait_asleep(uint64_t* bar, uint32_t parity,
     const unsigned long long t0 = global_timer_ns();
     while (!try_wait()) {
         if (*abort_flag) return false;
-        if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+        if (global_timer_ns() - t0 > limit_ns) {
             *abort_flag = 1;
             if (status) atomicOr(status, 1u);  // MOE_DEV_FLAG_TIMEOUT
             return false;
         }
     }
     return true;
+}
+
+// The limit of a wait for a tile's sums: a reduction of `steps` times 64 may take longer than
+// kWaitTimeoutNs by itself (2^30 rows of a weight gradient on one SM: 4.1 s, 0.25 us a step; wide
+// tiles of unaligned rows 0.8 us).
+__device__ __forceinline__ unsigned long long reduction_limit_ns(int steps) {
+    return kWaitTimeoutNs + static_cast<unsigned long long>(steps) * 2000ull;
 }
 
 // Bounded wait used only while tearing down after an abort (no flag, no status).

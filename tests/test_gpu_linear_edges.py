@@ -196,3 +196,22 @@ def test_training_codes_around_every_step(top, name):
         kept = (got + 0.5 - v).abs()
         assert bool((kept <= 0.5 + 2.0 ** -14).all())
         assert bool(((got >= 0) == (v >= 0))[v != 0].all())
+
+
+# -------------------------------------------------------------------------- the most rows
+def test_weight_gradient_of_the_most_rows():
+    """2^30 rows of one group: a single reduction of more than four seconds."""
+    rows = 1 << 30
+    x = torch.ones(rows, 8, dtype=bf, device="cuda")
+    dy = torch.zeros(rows, 8, dtype=bf, device="cuda")
+    dy[::4096] = 1
+    W = torch.zeros(1, 8, 8, dtype=bf, device="cuda")
+    ws = moe.alloc_grouped_linear_backward_workspace(rows, 8, 8, 1)
+    dW = torch.empty(1, 8, 8, device="cuda")
+    moe.moe_grouped_linear_backward(dy, x, None, W, ws, dW=dW)
+    assert moe.moe_device_status(ws) == 0
+    assert bool((dW == rows // 4096).all())
+    with pytest.raises(moe.MoeError):
+        moe.alloc_grouped_linear_backward_workspace(rows + 1, 8, 8, 1)
+    del x, dy, ws
+    torch.cuda.empty_cache()

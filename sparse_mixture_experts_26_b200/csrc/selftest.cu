@@ -9,7 +9,7 @@ namespace moe {
 namespace {
 
 // Block 0 waits on an mbarrier phase that never completes (the pipeline wait of the
-// GEMM kernels); block 1 waits for a device counter that nothing increments (the
+// GEMM kernels): first polling, then asleep, as the grouped linear kernels do.  Block 1 waits for a device counter that nothing increments (the
 // dependency wait of the fused small-batch FFN).  Both give up after limit_ns.
 __global__ void selftest_wait_kernel(uint32_t* status, const uint32_t* never_set,
                                      unsigned long long limit_ns, uint32_t* outcome) {
@@ -23,9 +23,13 @@ __global__ void selftest_wait_kernel(uint32_t* status, const uint32_t* never_set
     __syncthreads();
     if (threadIdx.x == 0) {
         bool ok;
-        if (blockIdx.x == 0)
+        if (blockIdx.x == 0) {
             ok = mbar_wait_bounded(&bar, 0, &abort_flag, status, limit_ns);
-        else
+            if (!ok && abort_flag == 1) {  // raised, so the next wait would give up at once
+                abort_flag = 0;
+                ok = mbar_wait_asleep(&bar, 0, &abort_flag, status, limit_ns) || abort_flag != 1;
+            }
+        } else
             ok = flag_wait_bounded(never_set, 1u, &abort_flag, status, limit_ns);
         outcome[blockIdx.x] = ok ? 1u : 2u;  // 2 = gave up, as it must
     }

@@ -1,11 +1,15 @@
 """Threads and driver contexts that call the tensor-map kernels: a thread without a context gets the
-device's primary one, a thread with one of its own keeps it.  In a process of its own, since contexts
-outlive a failing test."""
+device's primary one, a thread with one of its own keeps it (in a process of its own, since contexts
+outlive a failing test).  And the kernels' waits, which end when nothing arrives."""
 import os
 import subprocess
 import sys
+import time
 
 import pytest
+import torch
+
+import sparse_mixture_experts_26_b200 as moe
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -87,3 +91,14 @@ def test_contexts_of_calling_threads(body):
     run = subprocess.run([sys.executable, "-c", HEAD + body + "print('done')"], cwd=ROOT,
                          capture_output=True, text=True, timeout=300)
     assert run.returncode == 0 and run.stdout.strip() == "done", run.stderr
+
+
+def test_the_sleeping_wait_gives_up_too():
+    """The self-test's barrier is waited for twice, by polling and asleep, each up to the limit."""
+    ws = torch.zeros(4096, dtype=torch.uint8, device="cuda")
+    moe.moe_selftest_wait_timeout(ws, 0.01)  # the library is loaded
+    t0 = time.perf_counter()
+    assert moe.moe_selftest_wait_timeout(ws, 0.5) == (2, 2)
+    assert 1.0 <= time.perf_counter() - t0 < 5.0
+    assert moe.moe_device_status(ws) & 1 and moe.moe_device_status(ws) == 0
+    assert not bool(ws.any())

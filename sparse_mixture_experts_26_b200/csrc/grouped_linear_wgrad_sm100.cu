@@ -512,7 +512,8 @@ cudaError_t launch_typed(const LinearBwdArgs& a) {
     // (K 4096, N 14336, 8 groups: 256 rows 168 us against 182 with eight warps and four stages,
     // 512 rows 175 and 187, 1024 rows 206 and 198).  fp32 has half the values per byte and twice
     // the bytes, where more writers only scatter them (341 against 316 us).
-    if (!F32 && a.rows / a.E < kShortRows) return launch_wgrad<false, F32, 64, 3, 4>(a, l.width);
+    if constexpr (!F32)
+        if (a.rows / a.E < kShortRows) return launch_wgrad<false, F32, 64, 3, 4>(a, l.width);
     return launch_wgrad<false, F32, 64, 4, 2>(a, l.width);
 }
 

@@ -157,7 +157,6 @@ struct Args {
     int F;                // output features
     int C;                // reduction length
     int width;            // most token columns of a tile
-    int box;              // token rows per TMA box
     int group;            // token tiles whose rows stay in L2 together
     int act;
     const __nv_bfloat16* bias;

@@ -215,3 +215,27 @@ def test_weight_gradient_of_the_most_rows():
         moe.alloc_grouped_linear_backward_workspace(rows + 1, 8, 8, 1)
     del x, dy, ws
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("counts,K,N", [((5, 0, 20), 128, 136), ((300, 260), 128, 264),
+                                        ((1100, 900), 128, 264), ((5, 0, 3), 8192, 40)])
+@pytest.mark.parametrize("name", R.ACTS)
+def test_train_with_fp32_output(counts, K, N, name):
+    n = sum(counts)
+    t = R.inputs(counts, K, N, bf, 19, residual=True)
+    off = R.offsets_of(counts)
+    ws = moe.alloc_grouped_linear_workspace(n, K, N, len(counts))
+    y, y16 = torch.empty(n, N, device="cuda"), torch.empty(n, N, dtype=bf, device="cuda")
+    kept, kept16 = moe.alloc_checkpoint(n, N), moe.alloc_checkpoint(n, N)
+    for out, ck in ((y, kept), (y16, kept16)):
+        moe.moe_grouped_linear_train(t["x"], off, t["W"], out, *ck, ws, bias=t["bias"],
+                                     residual=t["residual"], act=name)
+    only = moe.grouped_linear(t["x"], off, t["W"], t["bias"], t["residual"], act=name, ws=ws,
+                              out=torch.empty_like(y))
+    assert torch.equal(y, only) and torch.equal(y.to(bf), y16)
+    assert all(torch.equal(a, b) for a, b in zip(kept, kept16))
+    z, mag = R.grouped_z(t["x"], t["W"], t["bias"], counts)
+    ref = R.act(z, name) + t["residual"].double()
+    # fp32 sums, the activation's own error, one rounding each
+    tol = R.SLOPE_MAX * R.accumulation(K) * mag + R.ACT_ERR * (1 + z.abs()) + 2.0 ** -23 * ref.abs()
+    assert bool(((y.double() - ref).abs() <= tol).all())

@@ -326,9 +326,9 @@ size_t moe_grouped_linear_workspace_bytes(int rows, int K, int N, int E, moe_dty
  *   y        [rows, N]  y_dt out
  * dt == MOE_BF16: tensor cores with fp32 accumulation, everything up to y in fp32 and
  * one rounding to y_dt (MOE_BF16, or MOE_F32 as moe_combine reads it); the GELU there is
- * made for a bf16 output, off by about 1e-7 |z| (4e-3 of itself at z = -6).  dt == MOE_F32:
- * fp32 throughout on CUDA cores, the activations within 6 units in the last place, y_dt ==
- * MOE_F32. */
+ * made for a bf16 output, off by about 1e-7 |z| (4e-3 of itself at z = -6, 3e-2 at -12).
+ * dt == MOE_F32: fp32 throughout on CUDA cores, the activations within 6 units in the last
+ * place, y_dt == MOE_F32. */
 moe_status moe_grouped_linear(const void *x, const int32_t *offsets, const void *W,
                               const void *bias, const void *residual, int rows, int K, int N,
                               int E, moe_act act, moe_dtype dt, moe_dtype y_dt, void *y, void *ws,

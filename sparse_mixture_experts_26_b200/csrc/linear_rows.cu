@@ -13,9 +13,10 @@
 // to the workspace, and the block that brings a group's last chunk adds them in chunk order
 // (whichever block that is, so db does not depend on the timing).  Without an activation dz
 // is dy itself: only the tails and db are made.
-// Measured at 8192 x 14336 with db (us; 600 MB): ReLU 117, SiLU 127, GELU 134; with chunks of
-// 64 rows 131, 142 and 160.  Small calls: one warp finds all groups' chunks with a scan (a walk
-// over the groups by every thread took 250 clocks a group: 32 groups, 150 x 144, 5.9 -> 2.4 us).
+// Measured at 8192 x 14336 with db (us; 600 MB): ReLU 115, SiLU 124, GELU 136 (with chunks of 64
+// rows 131, 142 and 160, of earlier forms of the slopes).  Small calls: one warp finds all groups'
+// chunks with a scan (a walk over the groups by every thread took 250 clocks a group: 32 groups,
+// 150 x 144, 5.9 -> 2.4 us).
 #include <cuda_bf16.h>
 
 #include "linear_device.cuh"

@@ -340,9 +340,9 @@ moe_status moe_grouped_linear(const void *x, const int32_t *offsets, const void 
  *   (q + 1/2) s:  codes [rows, N] int8, scales [rows, ceil(N / 32)] float.
  * The value is off by at most s / 2 = max|v| / 256, and its sign is kept (v >= 0 gives
  * q >= 0, v < 0 gives q < 0).  Zero itself has no code: beside other values it comes back as
- * s / 2, so values of which many are zero (a ReLU's output) gain an offset.  A block whose largest magnitude is below
- * 2^-100 is kept as zeros (s = 0); one that holds an infinity or NaN comes back as
- * infinities or NaN. */
+ * s / 2, so values of which many are zero (a ReLU's output) gain an offset.  A block whose
+ * largest magnitude is below 2^-100 is kept as zeros (s = 0); one that holds an infinity or
+ * NaN comes back as infinities or NaN. */
 #define MOE_CHECKPOINT_BLOCK 32
 
 /* moe_grouped_linear for training: the same y, and the pre-activations z kept as an
